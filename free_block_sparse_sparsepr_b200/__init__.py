@@ -8,6 +8,7 @@ missing, importing the binding's entry points raises.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import re
 
@@ -59,6 +60,13 @@ class Stats(ctypes.Structure):
                 ("device_status", ctypes.c_int)]
 
 
+class RopeConfig(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("H", ctypes.c_int), ("N", ctypes.c_int), ("d", ctypes.c_int),
+                ("layout", ctypes.c_int), ("axes", ctypes.c_int), ("dtype", ctypes.c_int), ("width", ctypes.c_int * 3),
+                ("stride_b", ctypes.c_longlong), ("stride_n", ctypes.c_longlong), ("stride_h", ctypes.c_longlong),
+                ("pos_stride_b", ctypes.c_longlong), ("amplitude", ctypes.c_double), ("freq", ctypes.c_double * 64)]
+
+
 class SparsePRError(RuntimeError):
     def __init__(self, fn: str, code: int):
         super().__init__(f"{fn} failed: {STATUS.get(code, code)} ({code})")
@@ -102,6 +110,13 @@ def load_library() -> ctypes.CDLL:
         "sparsepr_attention": (st, [H, _p, _p, _p, _p, _p]),
         "sparsepr_attention_host": (st, [H, _p, _p, _p, _p, _p]),
         "sparsepr_dense_attn": (st, [H, _p, _p, _p, _p, _p]),
+        "sparsepr_dense_attn_lse": (st, [H, _p, _p, _p, _p, _p, _p]),
+        "sparsepr_attn_bwd_workspace": (st, [H, ctypes.POINTER(ctypes.c_size_t)]),
+        "sparsepr_dense_attn_bwd": (st, [H] + [_p] * 10 + [ctypes.c_size_t, _p]),
+        "sparsepr_blocksparse_attn_bwd": (st, [H, _p, _p, _p, ctypes.POINTER(Partition), ctypes.POINTER(Route)]
+                                          + [_p] * 7 + [ctypes.c_size_t, _p]),
+        "sparsepr_rope": (st, [ctypes.POINTER(RopeConfig), _p, _p, _p, _p]),
+        "sparsepr_rope_bwd": (st, [ctypes.POINTER(RopeConfig), _p, _p, _p, _p]),
         "sparsepr_get_stats": (st, [H, ctypes.POINTER(Stats)]),
         "sparsepr_device_status": (st, [H, ctypes.POINTER(ctypes.c_int)]),
         "sparsepr_last_launch_count": (st, [H, ctypes.POINTER(ctypes.c_int)]),
@@ -143,6 +158,28 @@ def _stream(stream) -> int | None:
     return stream.cuda_stream
 
 
+def _on(device, stream):
+    """Context with `device` current and, if `stream` is given, that stream current too, so that
+    memory taken inside belongs to the stream that uses it."""
+    import contextlib
+
+    import torch
+
+    ctx = contextlib.ExitStack()
+    ctx.enter_context(torch.cuda.device(device))
+    if stream is not None:
+        ctx.enter_context(torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int)
+                                            else stream))
+    return ctx
+
+
+def _want(name, t, shape, dtype, device):
+    """Refuse a tensor argument that the C ABI would read or write wrongly."""
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor {tuple(shape)} on {device}, got {t.dtype} "
+                         f"{tuple(t.shape)} with strides {t.stride()} on {t.device}")
+
+
 class _DevArray:
     """Zero-copy __cuda_array_interface__ view of handle-owned device memory."""
 
@@ -170,6 +207,9 @@ class SparsePR:
         h = _p()
         _check("sparsepr_create", self.lib.sparsepr_create(ctypes.byref(self.cfg), ctypes.byref(h)))
         self.h = h
+        import torch
+
+        self.device = torch.device("cuda", torch.cuda.current_device())
 
     @classmethod
     def from_workload(cls, w, flags=0, **kw):
@@ -302,14 +342,71 @@ class SparsePR:
                                                                            _ptr(O), _stream(stream)))
         return O
 
-    def dense_attn(self, Q, K, V, O=None, stream=None):
+    def dense_attn(self, Q, K, V, O=None, stream=None, lse=None):
+        """Dense attention; with `lse` (fp32 [B, Hq, N]) the rows' log softmax denominators are written too."""
         if O is None:
             import torch
 
             O = torch.empty_like(Q)
-        _check("sparsepr_dense_attn", self.lib.sparsepr_dense_attn(self.h, _ptr(Q), _ptr(K), _ptr(V), _ptr(O),
-                                                                   _stream(stream)))
+        _check("sparsepr_dense_attn", self.lib.sparsepr_dense_attn_lse(self.h, _ptr(Q), _ptr(K), _ptr(V), _ptr(O),
+                                                                       _ptr(lse), _stream(stream)))
         return O
+
+    # ------------------------------------------------------------------ backward passes
+    def attn_bwd_workspace_bytes(self) -> int:
+        n = ctypes.c_size_t()
+        _check("sparsepr_attn_bwd_workspace", self.lib.sparsepr_attn_bwd_workspace(self.h, ctypes.byref(n)))
+        return n.value
+
+    def _bwd(self, name, call, Q, K, V, O, lse, dO, dQ, dK, dV, need_dq, need_dkv, workspace, stream):
+        import torch
+
+        c = self.cfg
+        qs, ks = (c.B, c.Hq, c.N, c.d), (c.B, c.Hkv, c.N, c.d)
+        if not need_dq and not need_dkv:
+            raise ValueError("no gradient asked for")
+        if (dQ is not None and not need_dq) or ((dK is not None or dV is not None) and not need_dkv):
+            raise ValueError("an output is given for a gradient that is not asked for")
+        for label, t, shape, dt in (("Q", Q, qs, torch.bfloat16), ("K", K, ks, torch.bfloat16), ("V", V, ks, torch.bfloat16),
+                                    ("O", O, qs, torch.bfloat16), ("lse", lse, qs[:3], torch.float32),
+                                    ("dO", dO, qs, torch.bfloat16)):
+            _want(label, t, shape, dt, self.device)
+        with _on(self.device, stream):
+            new = lambda shape: torch.empty(shape, dtype=torch.bfloat16, device=self.device)  # noqa: E731
+            if need_dq:
+                dQ = new(qs) if dQ is None else dQ
+                _want("dQ", dQ, qs, torch.bfloat16, self.device)
+            if need_dkv:
+                dK, dV = new(ks) if dK is None else dK, new(ks) if dV is None else dV
+                _want("dK", dK, ks, torch.bfloat16, self.device)
+                _want("dV", dV, ks, torch.bfloat16, self.device)
+            if workspace is None:
+                workspace = torch.empty(self.attn_bwd_workspace_bytes(), dtype=torch.uint8, device=self.device)
+            elif workspace.device != self.device or not workspace.is_contiguous():
+                raise ValueError(f"workspace: expected contiguous memory on {self.device}")
+            _check(name, call(_ptr(O), _ptr(lse), _ptr(dO), _ptr(dQ), _ptr(dK), _ptr(dV), _ptr(workspace),
+                              workspace.numel() * workspace.element_size(), _stream(stream)))
+        return dQ, dK, dV
+
+    def dense_attn_bwd(self, Q, K, V, O, lse, dO, dQ=None, dK=None, dV=None, need_dq=True, need_dkv=True,
+                       workspace=None, stream=None):
+        """Gradients (dQ, dK, dV) of dense_attn from its output O and lse and the gradient dO of O (None for
+        one that need_dq / need_dkv leave out). workspace: attn_bwd_workspace_bytes() of device memory that
+        a program may keep; None takes it from torch for this call."""
+        return self._bwd("sparsepr_dense_attn_bwd",
+                         lambda *a: self.lib.sparsepr_dense_attn_bwd(self.h, _ptr(Q), _ptr(K), _ptr(V), *a),
+                         Q, K, V, O, lse, dO, dQ, dK, dV, need_dq, need_dkv, workspace, stream)
+
+    def blocksparse_attn_bwd(self, Qp, Kp, Vp, part: Partition, route: Route, Osp, lse, dOsp, dQ=None, dK=None,
+                             dV=None, need_dq=True, need_dkv=True, workspace=None, stream=None):
+        """Gradients of permute followed by blocksparse_attn, with the partition and the route held constant:
+        group-major Qp, Kp, Vp, Osp, lse and dOsp in (dOsp: permute of the original-order gradient), dQ, dK
+        and dV in the original token order out. A partition or route whose buffers the handle owns is
+        overwritten by the handle's next call: keep copies (partition_views, route_views) across calls."""
+        return self._bwd("sparsepr_blocksparse_attn_bwd",
+                         lambda *a: self.lib.sparsepr_blocksparse_attn_bwd(
+                             self.h, _ptr(Qp), _ptr(Kp), _ptr(Vp), ctypes.byref(part), ctypes.byref(route), *a),
+                         Qp, Kp, Vp, Osp, lse, dOsp, dQ, dK, dV, need_dq, need_dkv, workspace, stream)
 
     # ------------------------------------------------------------------ introspection
     def stats(self) -> dict:
@@ -387,6 +484,117 @@ class SparsePR:
                 "Osp": device_view(fit.Osp, (Hp, c.M, c.d), torch.float32)}
 
 
+class Rope:
+    """Rotary positions of Q and K: from a model's token-major tensors into the head-major bf16
+    layout of the attention calls (`forward`), and the gradient back (`backward`).
+
+    widths  rotated elements of each axis, even: (w,) for a sequence (w < d rotates part of the head),
+            (frame, row, column) for video tokens
+    layout  "interleaved": pairs (2i, 2i + 1) of an axis' section; "half": pairs (i, i + w/2)
+    scaling "none": freq_i = base^(-2i/w)
+            "linear": freq_i / factor (positions interpolated into the trained range)
+            "ntk": base * factor^(w / (w - 2)) in place of base
+            "yarn": pairs that turn at least beta_fast times within trained_length keep freq_i, those that
+            turn at most beta_slow times take freq_i / factor, a linear ramp over the pair index between;
+            turned pairs are multiplied by 0.1 ln(factor) + 1
+    amplitude  factor of the turned pairs; None: the scaling's own"""
+
+    def __init__(self, d, widths, layout="half", base=10000.0, scaling="none", factor=1.0, trained_length=None,
+                 beta_fast=32.0, beta_slow=1.0, amplitude=None):
+        widths = tuple(int(w) for w in widths)
+        if d not in (64, 128):
+            raise ValueError(f"head dimension {d}: 64 or 128")
+        if not 1 <= len(widths) <= 3 or any(w < 2 or w % 2 for w in widths) or sum(widths) > d:
+            raise ValueError(f"widths {widths}: one to three even widths of at least 2, at most {d} together")
+        if layout not in ("interleaved", "half"):
+            raise ValueError(f"layout {layout!r}: 'interleaved' or 'half'")
+        if not base > 1.0 or not factor > 0.0:
+            raise ValueError("base must be above 1 and factor above 0")
+        if scaling == "yarn" and not (trained_length and trained_length > 0 and beta_fast > beta_slow > 0.0):
+            raise ValueError("yarn needs trained_length and beta_fast > beta_slow > 0")
+        self.d, self.widths = d, widths
+        self.layout = 0 if layout == "interleaved" else 1
+        self.freq = [f for w in widths for f in self._frequencies(w, float(base), scaling, float(factor),
+                                                                  trained_length, beta_fast, beta_slow)]
+        if amplitude is None:
+            amplitude = 0.1 * math.log(factor) + 1.0 if scaling == "yarn" else 1.0
+        self.amplitude = float(amplitude)
+        self.lib = load_library()
+
+    @staticmethod
+    def _frequencies(w, base, scaling, factor, trained, beta_fast, beta_slow):
+        if scaling == "ntk":
+            base = base * factor ** (w / max(w - 2, 1))
+        freq = [base ** (-2.0 * i / w) for i in range(w // 2)]
+        if scaling in ("none", "ntk"):
+            return freq
+        if scaling == "linear":
+            return [f / factor for f in freq]
+        if scaling != "yarn":
+            raise ValueError(f"scaling {scaling!r}: 'none', 'linear', 'ntk' or 'yarn'")
+
+        def pair(turns):   # index at which a pair turns that often within the trained length
+            return w * math.log(trained / (turns * 2.0 * math.pi)) / (2.0 * math.log(base))
+
+        lo, hi = max(math.floor(pair(beta_fast)), 0), min(math.ceil(pair(beta_slow)), w - 1)
+        slow = [min(max((i - lo) / max(hi - lo, 1e-3), 0.0), 1.0) for i in range(w // 2)]
+        return [f / factor * s + f * (1.0 - s) for f, s in zip(freq, slow)]
+
+    def _config(self, model, pos):
+        import torch
+
+        if model.dim() != 4 or model.shape[3] != self.d or model.stride(3) != 1 or 0 in model.shape:
+            raise ValueError(f"expected a token-major tensor [B, N, H, {self.d}] with contiguous heads, got "
+                             f"{tuple(model.shape)} with strides {model.stride()}")
+        if model.dtype not in (torch.bfloat16, torch.float32):
+            raise ValueError(f"token-major tensor of {model.dtype}: bfloat16 or float32")
+        B, N, H, d = model.shape
+        axes = len(self.widths)
+        if tuple(pos.shape) not in ((N, axes), (B, N, axes)) or pos.dtype != torch.int32 or not pos.is_contiguous() \
+                or pos.device != model.device:
+            raise ValueError(f"positions: expected a contiguous int32 tensor [{N}, {axes}] or [{B}, {N}, {axes}] on "
+                             f"{model.device}, got {pos.dtype} {tuple(pos.shape)} on {pos.device}")
+        if not model.is_cuda:
+            raise ValueError("tensors must be on a CUDA device")
+        return RopeConfig(B, H, N, d, self.layout, axes, 1 if model.dtype == torch.float32 else 0,
+                          (ctypes.c_int * 3)(*self.widths), model.stride(0), model.stride(1), model.stride(2),
+                          N * axes if pos.dim() == 3 else 0, self.amplitude, (ctypes.c_double * 64)(*self.freq))
+
+    def forward(self, x, pos, out=None, stream=None):
+        """x [B, N, H, d] bf16 or fp32 (any strides of 16-byte multiples, e.g. a slice of a fused projection)
+        turned by int32 positions [N, axes] or [B, N, axes]: bf16 [B, H, N, d]."""
+        import torch
+
+        cfg = self._config(x, pos)
+        shape = (cfg.B, cfg.H, cfg.N, cfg.d)
+        with _on(x.device, stream):
+            if out is None:
+                out = torch.empty(shape, dtype=torch.bfloat16, device=x.device)
+            _want("out", out, shape, torch.bfloat16, x.device)
+            _check("sparsepr_rope", self.lib.sparsepr_rope(ctypes.byref(cfg), _ptr(x), _ptr(pos), _ptr(out),
+                                                           _stream(stream)))
+        return out
+
+    def backward(self, dy, pos, out=None, dtype=None, stream=None):
+        """Gradient dy bf16 [B, H, N, d] of forward's output -> gradient of x, [B, N, H, d] of `dtype` (bf16
+        unless given) or written into `out` (any strides of 16-byte multiples whose rows do not overlap)."""
+        import torch
+
+        if dy.dim() != 4 or not dy.is_cuda or out is not None and dtype not in (None, out.dtype):
+            raise ValueError("dy must be [B, H, N, d] on a CUDA device, and dtype that of out")
+        B, H, N, d = dy.shape
+        _want("dy", dy, (B, H, N, d), torch.bfloat16, dy.device)
+        with _on(dy.device, stream):
+            if out is None:
+                out = torch.empty((B, N, H, d), dtype=dtype or torch.bfloat16, device=dy.device)
+            elif tuple(out.shape) != (B, N, H, d) or out.device != dy.device:
+                raise ValueError(f"out: expected [{B}, {N}, {H}, {d}] on {dy.device}, got {tuple(out.shape)} on {out.device}")
+            cfg = self._config(out, pos)
+            _check("sparsepr_rope_bwd", self.lib.sparsepr_rope_bwd(ctypes.byref(cfg), _ptr(dy), _ptr(pos), _ptr(out),
+                                                                   _stream(stream)))
+        return out
+
+
 def partition_from_tensors(t: dict) -> Partition:
     """Partition struct pointing at caller-owned device tensors (for handing a partition in)."""
     p = Partition()
@@ -405,7 +613,7 @@ def route_from_tensors(t: dict) -> Route:
     return r
 
 
-__all__ = ["SparsePR", "SparsePRError", "Config", "Partition", "Route", "Fit", "Stats", "load_library",
+__all__ = ["SparsePR", "Rope", "RopeConfig", "SparsePRError", "Config", "Partition", "Route", "Fit", "Stats", "load_library",
            "header_functions", "partition_from_tensors", "route_from_tensors", "device_view", "LIB_PATH",
            "FLAG_HARD_DROP_ONLY", "FLAG_RIDGE_ONLY", "FLAG_RBAR_UNPROJECTED", "FLAG_UNIFORM_WEIGHTS", "FLAG_TOPMASS",
            "FLAG_PROBES_UNIFORM", "FLAG_PROBES_RANDOM", "FLAG_SEMANTIC_PARTITION", "SHARED_ROWS",

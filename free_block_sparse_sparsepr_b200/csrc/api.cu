@@ -916,20 +916,106 @@ sparsepr_status sparsepr_attention_host(sparsepr_handle h, const void* Q, const 
 
 sparsepr_status sparsepr_dense_attn(sparsepr_handle h, const void* Q, const void* K, const void* V, void* O,
                                     void* stream) {
+    return sparsepr_dense_attn_lse(h, Q, K, V, O, nullptr, stream);
+}
+
+sparsepr_status sparsepr_dense_attn_lse(sparsepr_handle h, const void* Q, const void* K, const void* V, void* O,
+                                        float* lse, void* stream) {
+    if (lse && (reinterpret_cast<uintptr_t>(lse) & 3u) != 0) return SPARSEPR_ERR_INVALID_ARG;
     if (!h || !aligned16(Q) || !aligned16(K) || !aligned16(V) || !aligned16(O)) return SPARSEPR_ERR_INVALID_ARG;
     const sparsepr_config& c = h->cfg;
     h->launches = 0;
     if (spr::attn_tc_supported(c.d)) {
         SPR_TRY(spr::launch_attn_dense_tc(static_cast<const bf16*>(Q), static_cast<const bf16*>(K),
-                                          static_cast<const bf16*>(V), static_cast<bf16*>(O), nullptr, c.B, c.Hq,
+                                          static_cast<const bf16*>(V), static_cast<bf16*>(O), lse, c.B, c.Hq,
                                           c.Hkv, c.N, c.d, h->dev_status, (c.flags & SPARSEPR_FLAG_TEST_STALL) != 0,
                                           as_stream(stream)));
         return SPARSEPR_OK;
     }
     SPR_TRY(spr::launch_attn_dense(static_cast<const bf16*>(Q), static_cast<const bf16*>(K),
-                                   static_cast<const bf16*>(V), static_cast<bf16*>(O), nullptr, c.B, c.Hq, c.Hkv,
+                                   static_cast<const bf16*>(V), static_cast<bf16*>(O), lse, c.B, c.Hq, c.Hkv,
                                    c.N, c.d, as_stream(stream)));
     return SPARSEPR_OK;
+}
+
+namespace {
+
+// No output of a backward pass may meet an input or another output.
+bool bwd_overlap(sparsepr_handle h, const spr::AttnBwdArgs& a) {
+    const sparsepr_config& c = h->cfg;
+    const size_t qb = (size_t)h->Hp * c.N * c.d * sizeof(bf16), kb = (size_t)h->P * c.N * c.d * sizeof(bf16);
+    struct Range { const void* p; size_t n; };
+    const Range in[] = {{a.Q, qb}, {a.K, kb}, {a.V, kb}, {a.O, qb}, {a.dO, qb}, {a.lse, (size_t)h->Hp * c.N * sizeof(float)}};
+    const Range out[] = {{a.dQ, qb}, {a.dK, kb}, {a.dV, kb},
+                         {a.workspace, spr::attn_bwd_workspace(h->P, h->g, c.N, c.d, c.Gq, c.Gk, a.rowptr != nullptr)}};
+    auto meet = [](const Range& x, const Range& y) {
+        const uintptr_t u = reinterpret_cast<uintptr_t>(x.p), v = reinterpret_cast<uintptr_t>(y.p);
+        return x.p && y.p && u < v + y.n && v < u + x.n;
+    };
+    for (int i = 0; i < 4; ++i) {
+        for (const Range& r : in)
+            if (meet(out[i], r)) return true;
+        for (int j = 0; j < i; ++j)
+            if (meet(out[i], out[j])) return true;
+    }
+    return false;
+}
+
+sparsepr_status attn_bwd_impl(sparsepr_handle h, const void* Q, const void* K, const void* V,
+                              const sparsepr_partition_t* part, const sparsepr_route_t* route, const void* O,
+                              const float* lse, const void* dO, void* dQ, void* dK, void* dV, void* workspace,
+                              size_t workspace_bytes, void* stream) {
+    if (!aligned16(Q) || !aligned16(K) || !aligned16(V) || !aligned16(O) || !aligned16(dO) || !aligned16(workspace))
+        return SPARSEPR_ERR_INVALID_ARG;
+    if (!lse || (reinterpret_cast<uintptr_t>(lse) & 3u) != 0) return SPARSEPR_ERR_INVALID_ARG;
+    if ((dQ && !aligned16(dQ)) || (dK && !aligned16(dK)) || (dV && !aligned16(dV)) || !dK != !dV || (!dQ && !dK))
+        return SPARSEPR_ERR_INVALID_ARG;
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev != h->device) return SPARSEPR_ERR_INVALID_ARG;
+    const sparsepr_config& c = h->cfg;
+    if (workspace_bytes < spr::attn_bwd_workspace(h->P, h->g, c.N, c.d, c.Gq, c.Gk, route != nullptr))
+        return SPARSEPR_ERR_WORKSPACE;
+    spr::AttnBwdArgs a;
+    memset(&a, 0, sizeof(a));
+    a.Q = static_cast<const bf16*>(Q); a.K = static_cast<const bf16*>(K); a.V = static_cast<const bf16*>(V);
+    a.O = static_cast<const bf16*>(O); a.dO = static_cast<const bf16*>(dO); a.lse = lse;
+    a.dQ = static_cast<bf16*>(dQ); a.dK = static_cast<bf16*>(dK); a.dV = static_cast<bf16*>(dV);
+    a.workspace = workspace;
+    a.status = h->dev_status;
+    a.P = h->P; a.g = h->g; a.N = c.N; a.d = c.d; a.Gq = c.Gq; a.Gk = c.Gk;
+    if (route) {
+        a.qperm = part->qperm; a.kperm = part->kperm; a.qoff = part->qoff; a.koff = part->koff;
+        a.rowptr = route->rowptr; a.kg = route->kg;
+    }
+    if (bwd_overlap(h, a)) return SPARSEPR_ERR_INVALID_ARG;
+    h->launches = 0;
+    if (spr::launch_attn_bwd(a, as_stream(stream)) != cudaSuccess) return SPARSEPR_ERR_CUDA;
+    h->launches = spr::attn_bwd_launches(a);
+    return SPARSEPR_OK;
+}
+
+}  // namespace
+
+sparsepr_status sparsepr_attn_bwd_workspace(sparsepr_handle h, size_t* bytes) {
+    if (!h || !bytes) return SPARSEPR_ERR_INVALID_ARG;
+    *bytes = spr::attn_bwd_workspace(h->P, h->g, h->cfg.N, h->cfg.d, h->cfg.Gq, h->cfg.Gk, true);
+    return SPARSEPR_OK;
+}
+
+sparsepr_status sparsepr_dense_attn_bwd(sparsepr_handle h, const void* Q, const void* K, const void* V, const void* O,
+                                        const float* lse, const void* dO, void* dQ, void* dK, void* dV,
+                                        void* workspace, size_t workspace_bytes, void* stream) {
+    if (!h) return SPARSEPR_ERR_INVALID_ARG;
+    return attn_bwd_impl(h, Q, K, V, nullptr, nullptr, O, lse, dO, dQ, dK, dV, workspace, workspace_bytes, stream);
+}
+
+sparsepr_status sparsepr_blocksparse_attn_bwd(sparsepr_handle h, const void* Qp, const void* Kp, const void* Vp,
+                                              const sparsepr_partition_t* part, const sparsepr_route_t* route,
+                                              const void* Osp, const float* lse, const void* dOsp, void* dQ, void* dK,
+                                              void* dV, void* workspace, size_t workspace_bytes, void* stream) {
+    if (!h || !part || !part->kperm || !part->koff || !part->qperm || !part->qoff) return SPARSEPR_ERR_INVALID_ARG;
+    if (!route || !route->rowptr || !route->kg) return SPARSEPR_ERR_INVALID_ARG;
+    return attn_bwd_impl(h, Qp, Kp, Vp, part, route, Osp, lse, dOsp, dQ, dK, dV, workspace, workspace_bytes, stream);
 }
 
 sparsepr_status sparsepr_get_stats(sparsepr_handle h, sparsepr_stats* out) {

@@ -183,6 +183,24 @@ cudaError_t launch_attn_probe(const bf16* Q, const bf16* K, const bf16* V, const
                               float* Opart, float* mpart, float* lpart, float* Odense, int B,
                               int Hq, int Hkv, int N, int d, int M, int ns, cudaStream_t s);
 
+// ---------------------------------------------------------------- backward passes
+// Gradients of the dense (rowptr null) or block-sparse attention over P = B*Hkv KV heads of g query
+// heads each. Q, K, V, O, lse and dO as the forward pass takes and leaves them (group-major for the
+// block-sparse pass); dQ, dK, dV in original order (row qperm / kperm of each position). dQ null
+// skips it, dK and dV null skips both. workspace: attn_bwd_workspace bytes, 256-byte aligned parts.
+struct AttnBwdArgs {
+    const bf16 *Q, *K, *V, *O, *dO;
+    const float* lse;
+    const int32_t *qperm, *kperm, *qoff, *koff, *rowptr, *kg;
+    bf16 *dQ, *dK, *dV;
+    void* workspace;
+    int* status;
+    int P, g, N, d, Gq, Gk;
+};
+size_t attn_bwd_workspace(int P, int g, int N, int d, int Gq, int Gk, bool sparse);
+int attn_bwd_launches(const AttnBwdArgs& a);
+cudaError_t launch_attn_bwd(const AttnBwdArgs& a, cudaStream_t s);
+
 // ---------------------------------------------------------------- probe fit + write-back
 cudaError_t launch_probe_residual(const float* Odense, const bf16* Osp, const int32_t* probe_pos,
                                   float* R, float* Osp_probe, int Hp, int g, int N, int d, int M,

@@ -356,6 +356,89 @@ sparsepr_status sparsepr_dense_attn(sparsepr_handle h, const void* Q, const void
                                     void* O, void* stream);
 
 /*
+ * sparsepr_dense_attn that also writes lse: fp32 [B][Hq][N] natural-log softmax denominators of
+ * the scaled logits (NULL: not written), as sparsepr_dense_attn_bwd reads them.
+ */
+sparsepr_status sparsepr_dense_attn_lse(sparsepr_handle h, const void* Q, const void* K, const void* V,
+                                        void* O, float* lse, void* stream);
+
+/*
+ * Backward passes of the two attention calls, for training through them. The probabilities
+ * P = exp(q.k/sqrt(d) - lse) are recomputed from lse; with D = dO.O per row and
+ * dS = P (dO.v - D): dV = P^T dO, dK = dS^T Q / sqrt(d), dQ = dS K / sqrt(d), dK and dV summed over
+ * the query heads that share the KV head. Logits, sums and dS are fp32; P and dS are rounded to
+ * bf16 as matrix operands; every gradient is rounded to bf16 once. Results repeat bit for bit.
+ *
+ * sparsepr_dense_attn_bwd: Q, K, V, O, lse as sparsepr_dense_attn_lse takes and leaves them, dO the
+ * gradient of O; dQ bf16 [B][Hq][N][d], dK and dV bf16 [B][Hkv][N][d].
+ *
+ * sparsepr_blocksparse_attn_bwd: Qp, Kp, Vp, part, route, Osp, lse as sparsepr_blocksparse_attn takes
+ * and leaves them, dOsp the gradient of Osp in the same group-major order (sparsepr_permute of the
+ * original-order gradient); partition and route are constants. dQ, dK and dV are the gradients of
+ * the Q, K, V that sparsepr_permute gathered, in the ORIGINAL token order. A query row without kept
+ * keys (lse = -inf) has dQ = 0 and adds nothing; a key that no query group keeps has dK = dV = 0.
+ * Only kperm, koff, qperm and qoff of `part` and rowptr and kg of `route` are read. Ids, offsets
+ * and permutation entries out of range are skipped and reported as SPARSEPR_ERR_DEVICE in the
+ * device status word.
+ *
+ * dQ may be NULL, or dK and dV both, to leave those gradients out. No output may overlap an input
+ * or another output. workspace: caller-owned device memory, 16-byte aligned, of at least
+ * sparsepr_attn_bwd_workspace bytes (enough for either call), used until the call's work has
+ * finished; calls with different workspaces may overlap. Nothing else of the handle is written but
+ * the device status word, and the calls can be captured into a graph.
+ * SPARSEPR_ERR_WORKSPACE: workspace too small. SPARSEPR_ERR_INVALID_ARG also when the handle's
+ * device is not the current one.
+ */
+sparsepr_status sparsepr_attn_bwd_workspace(sparsepr_handle h, size_t* bytes);
+sparsepr_status sparsepr_dense_attn_bwd(sparsepr_handle h, const void* Q, const void* K, const void* V,
+                                        const void* O, const float* lse, const void* dO, void* dQ, void* dK,
+                                        void* dV, void* workspace, size_t workspace_bytes, void* stream);
+sparsepr_status sparsepr_blocksparse_attn_bwd(sparsepr_handle h, const void* Qp, const void* Kp, const void* Vp,
+                                              const sparsepr_partition_t* part, const sparsepr_route_t* route,
+                                              const void* Osp, const float* lse, const void* dOsp, void* dQ,
+                                              void* dK, void* dV, void* workspace, size_t workspace_bytes,
+                                              void* stream);
+
+/*
+ * Rotary positions of Q or K, from a model's token-major tensor into the head-major bf16 layout
+ * the attention calls read, and the gradient back. The first width[0] elements of every head turn
+ * with the token's coordinate on axis 0, the next width[1] with axis 1, and so on (frame, row and
+ * column of a video token; one axis for a plain sequence); elements past them pass through. Pair i
+ * of an axis' section is elements (2i, 2i + 1) (INTERLEAVED) or (i, i + width/2) (HALF) of it; a pair
+ * (u, v) at coordinate c becomes amplitude * (u cos t - v sin t, u sin t + v cos t), t = c freq[i].
+ *   B, H, N, d      samples, heads of this tensor, tokens, head dim (64 or 128)
+ *   axes, width     1..3 axes; even widths >= 2 whose sum is at most d
+ *   freq            radians per coordinate step of every pair, the axes' sections one after another
+ *                   (width/2 each); scaled frequencies of long contexts go in here. Angles are
+ *                   reduced in 64-bit fixed point, so they stay exact at any 32-bit coordinate
+ *   amplitude       factor of the turned pairs (1, or the attention factor of a scaled context)
+ *   dtype           element type of the token-major side: SPARSEPR_BF16 or SPARSEPR_FP32
+ *   stride_b/n/h    strides of the token-major side in elements, multiples of 16 bytes, e.g. of a
+ *                   slice of a fused projection (the stride of a dimension of size 1 is ignored)
+ *   pos_stride_b    elements from one sample's coordinates to the next's (0: shared by all)
+ * sparsepr_rope:     X token-major -> Y bf16 [B][H][N][d]
+ * sparsepr_rope_bwd: dY bf16 [B][H][N][d] -> dX token-major, the transposed map; rows of dX must
+ *                    not overlap one another
+ * pos: int32 [B or 1][N][axes], device. Source and destination must not overlap; both start on 16
+ * bytes. Results are rounded once. No handle, no workspace; runs on the current device.
+ */
+#define SPARSEPR_ROPE_INTERLEAVED 0
+#define SPARSEPR_ROPE_HALF 1
+#define SPARSEPR_BF16 0
+#define SPARSEPR_FP32 1
+typedef struct sparsepr_rope_config {
+    int B, H, N, d;
+    int layout, axes, dtype;
+    int width[3];
+    long long stride_b, stride_n, stride_h, pos_stride_b;
+    double amplitude;
+    double freq[64];
+} sparsepr_rope_config;
+sparsepr_status sparsepr_rope(const sparsepr_rope_config* cfg, const void* X, const int32_t* pos, void* Y, void* stream);
+sparsepr_status sparsepr_rope_bwd(const sparsepr_rope_config* cfg, const void* dY, const int32_t* pos, void* dX,
+                                  void* stream);
+
+/*
  * Statistics of the last sparsepr_attention / sparsepr_route call on the
  * handle. Waits for that call's work to finish (event synchronisation).
  */
