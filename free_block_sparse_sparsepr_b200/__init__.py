@@ -7,6 +7,7 @@ missing, importing the binding's entry points raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -161,10 +162,10 @@ def _stream(stream) -> int | None:
 def _on(device, stream):
     """Context with `device` current and, if `stream` is given, that stream current too, so that
     memory taken inside belongs to the stream that uses it."""
-    import contextlib
-
     import torch
 
+    if stream is None and device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
     ctx = contextlib.ExitStack()
     ctx.enter_context(torch.cuda.device(device))
     if stream is not None:
@@ -520,6 +521,8 @@ class Rope:
             amplitude = 0.1 * math.log(factor) + 1.0 if scaling == "yarn" else 1.0
         self.amplitude = float(amplitude)
         self.lib = load_library()
+        self._base = RopeConfig(0, 0, 0, d, self.layout, len(widths), 0, (ctypes.c_int * 3)(*widths), 0, 0, 0, 0,
+                                self.amplitude, (ctypes.c_double * 64)(*self.freq))
 
     @staticmethod
     def _frequencies(w, base, scaling, factor, trained, beta_fast, beta_slow):
@@ -556,9 +559,11 @@ class Rope:
                              f"{model.device}, got {pos.dtype} {tuple(pos.shape)} on {pos.device}")
         if not model.is_cuda:
             raise ValueError("tensors must be on a CUDA device")
-        return RopeConfig(B, H, N, d, self.layout, axes, 1 if model.dtype == torch.float32 else 0,
-                          (ctypes.c_int * 3)(*self.widths), model.stride(0), model.stride(1), model.stride(2),
-                          N * axes if pos.dim() == 3 else 0, self.amplitude, (ctypes.c_double * 64)(*self.freq))
+        c = RopeConfig.from_buffer_copy(self._base)      # one per call: calls of several threads do not meet
+        c.B, c.H, c.N, c.dtype = B, H, N, 1 if model.dtype == torch.float32 else 0
+        c.stride_b, c.stride_n, c.stride_h, _ = model.stride()
+        c.pos_stride_b = N * axes if pos.dim() == 3 else 0
+        return c
 
     def forward(self, x, pos, out=None, stream=None):
         """x [B, N, H, d] bf16 or fp32 (any strides of 16-byte multiples, e.g. a slice of a fused projection)

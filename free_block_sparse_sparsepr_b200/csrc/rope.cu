@@ -9,6 +9,8 @@
 #include <math.h>
 #include <string.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "kernels.h"
 #include "sparsepr.h"
@@ -17,52 +19,180 @@ namespace spr {
 namespace {
 
 constexpr int kMaxPairs = 64;
+constexpr int kThreads = 256;
 
 struct RopeParams {
     unsigned long long turn[kMaxPairs];   // freq / 2 pi modulo 1, as a fraction of 2^64
-    uint8_t axis[kMaxPairs], first[kMaxPairs], second[kMaxPairs];
+    uint8_t axis[kMaxPairs];
+    uint8_t first[kMaxPairs], second[kMaxPairs];      // the pairs' elements
+    uint8_t vec_a[8], vec_b[8], base[8];  // vector kernel: a thread's two 8-element vectors and its first pair
     long long sb, sn, sh, spos;           // token-major strides; batch stride of the positions
     const int32_t* pos;
+    const void* src;
+    void* dst;
     int H, N, axes, pairs;
+    int tokens, slots, heads;             // per block: tokens, heads at a time, heads in all
     float amplitude;
 };
 
-// One warp per (b, n, h) row.
-template <typename T, int D, bool BWD>
-__global__ void __launch_bounds__(256) rope_kernel(const RopeParams p, const void* src_, void* dst_, long long rows) {
-    const long long r = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-    const int lane = threadIdx.x & 31;
-    if (r >= rows) return;
-    const int h = (int)(r % p.H);
-    const long long bn = r / p.H;
-    const int n = (int)(bn % p.N), b = (int)(bn / p.N);
-    const long long model = b * p.sb + n * p.sn + h * p.sh, head = (((long long)b * p.H + h) * p.N + n) * D;
-    auto load = [&](int e) {
-        if (BWD) return bf16_to_f32(static_cast<const bf16*>(src_)[head + e]);
-        return (float)static_cast<const T*>(src_)[model + e];
-    };
-    auto store = [&](int e, float v) {
-        if (BWD) static_cast<T*>(dst_)[model + e] = (T)v;
-        else static_cast<bf16*>(dst_)[head + e] = __float2bfloat16_rn(v);
-    };
-    for (int i = lane; i < p.pairs; i += 32) {
-        const int32_t at = p.pos[b * p.spos + (long long)n * p.axes + p.axis[i]];
-        const long long turns = (long long)((unsigned long long)(long long)at * p.turn[i]);
-        float sn, cs;
-        sincospif((float)(int32_t)(turns >> 32) * 4.656612873077393e-10f, &sn, &cs);   // 2^-31: half turns
-        if (BWD) sn = -sn;
-        const float u = load(p.first[i]), v = load(p.second[i]);
-        store(p.first[i], p.amplitude * (u * cs - v * sn));
-        store(p.second[i], p.amplitude * (u * sn + v * cs));
+// amplitude * (cos, sin) of pair i at the token whose coordinates are `at`; sin negated for the
+// transposed map.
+template <bool BWD>
+__device__ __forceinline__ void turn_of(const RopeParams& p, int i, const int32_t* at, float& cs, float& sn) {
+    const long long t = (long long)((unsigned long long)(long long)at[p.axis[i]] * p.turn[i]);
+    sincospif((float)(int32_t)(t >> 32) * 4.656612873077393e-10f, &sn, &cs);   // 2^-31: half turns
+    cs *= p.amplitude;
+    sn *= BWD ? -p.amplitude : p.amplitude;
+}
+
+// Eight consecutive elements as fp32.
+__device__ __forceinline__ void load8(const bf16* p, float (&v)[8]) {
+    const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
-    for (int e = 2 * p.pairs + lane; e < D; e += 32) store(e, load(e));
+}
+__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+__device__ __forceinline__ void store8(bf16* p, const float (&v)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+
+// A thread's token and first head of the block, its last head, and the addresses of both sides.
+template <typename T, int D, bool BWD>
+struct Walk {
+    using Src = typename std::conditional<BWD, bf16, T>::type;
+    using Dst = typename std::conditional<BWD, T, bf16>::type;
+    const Src* src;
+    Dst* dst;
+    const int32_t* at;
+    long long src_step, dst_step;   // per head
+    int h, end;
+    bool any;
+    __device__ __forceinline__ Walk(const RopeParams& p, int row) {
+        const int n = blockIdx.x * p.tokens + row % p.tokens, b = blockIdx.y;
+        h = blockIdx.z * p.heads + row / p.tokens;
+        end = min(p.H, (blockIdx.z + 1) * p.heads);
+        any = n < p.N && h < end;
+        const long long model = b * p.sb + n * p.sn, head = ((long long)b * p.H * p.N + n) * D;
+        src = static_cast<const Src*>(p.src) + (BWD ? head : model);
+        dst = static_cast<Dst*>(p.dst) + (BWD ? model : head);
+        src_step = BWD ? (long long)p.N * D : p.sh;
+        dst_step = BWD ? p.sh : (long long)p.N * D;
+        at = p.pos + b * p.spos + (long long)n * p.axes;
+    }
+};
+
+// Vector kernel: a thread holds 16 elements (two 16-byte bf16 vectors, eight whole pairs) of a
+// token's head and walks over the block's heads with the angles in registers.
+template <typename T, int D, bool HALF, bool BWD>
+__global__ void __launch_bounds__(kThreads) rope_vec_kernel(const __grid_constant__ RopeParams p) {
+    constexpr int kUnits = D / 16;
+    const int u = threadIdx.x % kUnits;
+    Walk<T, D, BWD> w(p, threadIdx.x / kUnits);
+    if (!w.any) return;
+    const int a = 8 * p.vec_a[u], b = 8 * p.vec_b[u], first = p.base[u];
+    float cs[8], sn[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        cs[i] = 1.f;
+        sn[i] = 0.f;
+        if (first + i < p.pairs) turn_of<BWD>(p, first + i, w.at, cs[i], sn[i]);
+    }
+    const bool turned = first < p.pairs;
+#pragma unroll 2
+    for (int h = w.h; h < w.end; h += p.slots) {
+        float x[8], y[8];
+        load8(w.src + h * w.src_step + a, x);
+        load8(w.src + h * w.src_step + b, y);
+        if (turned) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (HALF) {
+                    const float v = x[i];
+                    x[i] = v * cs[i] - y[i] * sn[i];
+                    y[i] = v * sn[i] + y[i] * cs[i];
+                } else if (first + i < p.pairs) {
+                    float* q = i < 4 ? x + 2 * i : y + 2 * (i - 4);
+                    const float v = q[0];
+                    q[0] = v * cs[i] - q[1] * sn[i];
+                    q[1] = v * sn[i] + q[1] * cs[i];
+                }
+            }
+        }
+        store8(w.dst + h * w.dst_step + a, x);
+        store8(w.dst + h * w.dst_step + b, y);
+    }
+}
+
+// Scalar kernel, for half layouts whose sections do not split into vectors: a lane holds pairs
+// `lane` and `lane + 32` of a token's head, consecutive lanes consecutive elements.
+template <typename T, int D, bool BWD>
+__global__ void __launch_bounds__(kThreads) rope_scalar_kernel(const __grid_constant__ RopeParams p) {
+    const int lane = threadIdx.x & 31;
+    Walk<T, D, BWD> w(p, threadIdx.x >> 5);
+    if (!w.any) return;
+    float cs[2], sn[2];
+    int a[2], b[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const int i = lane + 32 * j;
+        cs[j] = 1.f;
+        sn[j] = 0.f;
+        // past the pairs: elements that pass through, two at a time
+        a[j] = i < p.pairs ? p.first[i] : 2 * i;
+        b[j] = i < p.pairs ? p.second[i] : 2 * i + 1;
+        if (i < p.pairs) turn_of<BWD>(p, i, w.at, cs[j], sn[j]);
+    }
+#pragma unroll 4
+    for (int h = w.h; h < w.end; h += p.slots) {
+        const auto* s = w.src + h * w.src_step;
+        auto* d = w.dst + h * w.dst_step;
+#pragma unroll
+        for (int j = 0; j < D / 64; ++j) {
+            const float x = (float)s[a[j]], y = (float)s[b[j]];
+            const bool turned = lane + 32 * j < p.pairs;
+            d[a[j]] = turned ? x * cs[j] - y * sn[j] : x;
+            d[b[j]] = turned ? x * sn[j] + y * cs[j] : y;
+        }
+    }
 }
 
 template <typename T, int D>
-void launch(const RopeParams& p, const void* src, void* dst, long long rows, bool bwd, cudaStream_t s) {
-    const unsigned blocks = (unsigned)((rows * 32 + 255) / 256);
-    if (bwd) rope_kernel<T, D, true><<<blocks, 256, 0, s>>>(p, src, dst, rows);
-    else rope_kernel<T, D, false><<<blocks, 256, 0, s>>>(p, src, dst, rows);
+void launch(RopeParams& p, int B, bool half, bool vec, bool bwd, int sms, cudaStream_t s) {
+    // A block has rows of (token, head) to hand out: up to 32 (vector) or 8 (scalar) tokens; with
+    // fewer tokens than that, the other rows take further heads. A block walks over as many heads
+    // as leave four blocks per SM, so that the angles of a token are formed once for all of them
+    // and a few tokens still spread over the GPU.
+    const int rows = vec ? kThreads / (D / 16) : kThreads / 32;
+    p.tokens = rows;
+    while (p.tokens / 2 >= p.N) p.tokens /= 2;
+    p.slots = rows / p.tokens;
+    const long long groups = (long long)B * ((p.N + p.tokens - 1) / p.tokens);
+    long long heads = groups * p.H / (4ll * sms);
+    heads = heads < 1 ? 1 : heads > p.H ? p.H : heads;
+    heads = (heads + p.slots - 1) / p.slots * p.slots;
+    p.heads = (int)heads;
+    const dim3 grid((unsigned)((p.N + p.tokens - 1) / p.tokens), (unsigned)B, (unsigned)((p.H + heads - 1) / heads));
+    if (!vec) bwd ? rope_scalar_kernel<T, D, true><<<grid, kThreads, 0, s>>>(p) : rope_scalar_kernel<T, D, false><<<grid, kThreads, 0, s>>>(p);
+    else if (half) bwd ? rope_vec_kernel<T, D, true, true><<<grid, kThreads, 0, s>>>(p) : rope_vec_kernel<T, D, true, false><<<grid, kThreads, 0, s>>>(p);
+    else bwd ? rope_vec_kernel<T, D, false, true><<<grid, kThreads, 0, s>>>(p) : rope_vec_kernel<T, D, false, false><<<grid, kThreads, 0, s>>>(p);
 }
 
 // Do the byte ranges [a, a + na) and [b, b + nb) meet?
@@ -88,16 +218,16 @@ sparsepr_status rope(const sparsepr_rope_config* c, const void* src, const int32
         sum += c->width[a];
     }
     if (sum > c->d) return SPARSEPR_ERR_INVALID_ARG;
-    const int vec = c->dtype == SPARSEPR_FP32 ? 4 : 8, size = 16 / vec;
+    const int per16 = c->dtype == SPARSEPR_FP32 ? 4 : 8, size = 16 / per16;
     if (c->pos_stride_b < 0) return SPARSEPR_ERR_INVALID_ARG;
     const long long size_of[3] = {c->B, c->N, c->H}, stride_of[3] = {c->stride_b, c->stride_n, c->stride_h};
     const long long rows = (long long)c->B * c->N;
-    if (rows > (1ll << 31) || rows * c->H > (1ll << 31)) return SPARSEPR_ERR_UNSUPPORTED;
+    if (c->B > 65535 || c->H > 65535 || rows > (1ll << 31) || rows * c->H > (1ll << 31)) return SPARSEPR_ERR_UNSUPPORTED;
     // every row of the token-major side starts on 16 bytes
     long long extent = c->d;
     for (int i = 0; i < 3; ++i) {
         if (size_of[i] == 1) continue;
-        if (stride_of[i] < 0 || stride_of[i] % vec != 0) return SPARSEPR_ERR_INVALID_ARG;
+        if (stride_of[i] < 0 || stride_of[i] % per16 != 0) return SPARSEPR_ERR_INVALID_ARG;
         if (stride_of[i] > (1ll << 40)) return SPARSEPR_ERR_UNSUPPORTED;
         extent += (size_of[i] - 1) * stride_of[i];
     }
@@ -143,13 +273,45 @@ sparsepr_status rope(const sparsepr_rope_config* c, const void* src, const int32
     p.sb = c->B > 1 ? c->stride_b : 0; p.sn = c->N > 1 ? c->stride_n : 0; p.sh = c->H > 1 ? c->stride_h : 0;
     p.spos = c->B > 1 ? c->pos_stride_b : 0;
     p.pos = pos;
+    p.src = src;
+    p.dst = dst;
     p.H = c->H; p.N = c->N; p.axes = c->axes;
     p.amplitude = (float)c->amplitude;
+    // Units of 16 elements for the vector kernel. Interleaved: 16 consecutive elements. Half: a vector
+    // and its partner, where every section's halves are whole vectors.
+    const bool half = c->layout == SPARSEPR_ROPE_HALF;
+    bool vec = true;
+    if (half) {
+        int unit = 0, start = 0, pair = 0;
+        for (int a = 0; a < c->axes; ++a) {
+            const int w = c->width[a];
+            if (w % 16 != 0) vec = false;
+            for (int i = 0; vec && i < w / 16; ++i, ++unit, pair += 8) {
+                p.vec_a[unit] = (uint8_t)(start / 8 + i);
+                p.vec_b[unit] = (uint8_t)(start / 8 + w / 16 + i);
+                p.base[unit] = (uint8_t)pair;
+            }
+            start += w;
+        }
+        for (int e = start / 8; vec && e < c->d / 8; e += 2, ++unit) {
+            p.vec_a[unit] = (uint8_t)e;
+            p.vec_b[unit] = (uint8_t)(e + 1);
+            p.base[unit] = (uint8_t)p.pairs;
+        }
+    } else {
+        for (int u = 0; u < c->d / 16; ++u) {
+            p.vec_a[u] = (uint8_t)(2 * u);
+            p.vec_b[u] = (uint8_t)(2 * u + 1);
+            p.base[u] = (uint8_t)(8 * u);
+        }
+    }
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return SPARSEPR_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const long long n = rows * c->H;
     const bool f32 = c->dtype == SPARSEPR_FP32;
-    if (c->d == 128) f32 ? launch<float, 128>(p, src, dst, n, bwd, s) : launch<bf16, 128>(p, src, dst, n, bwd, s);
-    else f32 ? launch<float, 64>(p, src, dst, n, bwd, s) : launch<bf16, 64>(p, src, dst, n, bwd, s);
+    if (c->d == 128) f32 ? launch<float, 128>(p, c->B, half, vec, bwd, sms, s) : launch<bf16, 128>(p, c->B, half, vec, bwd, sms, s);
+    else f32 ? launch<float, 64>(p, c->B, half, vec, bwd, sms, s) : launch<bf16, 64>(p, c->B, half, vec, bwd, sms, s);
     return cudaGetLastError() == cudaSuccess ? SPARSEPR_OK : SPARSEPR_ERR_CUDA;
 }
 
