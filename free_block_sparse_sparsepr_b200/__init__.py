@@ -174,9 +174,18 @@ def _on(device, stream):
     return ctx
 
 
+def _stream_on(device, stream) -> int:
+    """_stream on a given device (looking that device up anew costs microseconds a call)."""
+    if stream is None:
+        import torch
+
+        return torch.cuda.current_stream(device.index).cuda_stream
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
 def _want(name, t, shape, dtype, device):
     """Refuse a tensor argument that the C ABI would read or write wrongly."""
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device or not t.is_contiguous():
+    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous {dtype} tensor {tuple(shape)} on {device}, got {t.dtype} "
                          f"{tuple(t.shape)} with strides {t.stride()} on {t.device}")
 
@@ -211,6 +220,7 @@ class SparsePR:
         import torch
 
         self.device = torch.device("cuda", torch.cuda.current_device())
+        self._bwd_bytes = self.attn_bwd_workspace_bytes()
 
     @classmethod
     def from_workload(cls, w, flags=0, **kw):
@@ -363,30 +373,35 @@ class SparsePR:
         import torch
 
         c = self.cfg
-        qs, ks = (c.B, c.Hq, c.N, c.d), (c.B, c.Hkv, c.N, c.d)
+        B, Hq, Hkv, N, d = c.B, c.Hq, c.Hkv, c.N, c.d
+        qs, ks = (B, Hq, N, d), (B, Hkv, N, d)
         if not need_dq and not need_dkv:
             raise ValueError("no gradient asked for")
         if (dQ is not None and not need_dq) or ((dK is not None or dV is not None) and not need_dkv):
             raise ValueError("an output is given for a gradient that is not asked for")
-        for label, t, shape, dt in (("Q", Q, qs, torch.bfloat16), ("K", K, ks, torch.bfloat16), ("V", V, ks, torch.bfloat16),
-                                    ("O", O, qs, torch.bfloat16), ("lse", lse, qs[:3], torch.float32),
-                                    ("dO", dO, qs, torch.bfloat16)):
-            _want(label, t, shape, dt, self.device)
-        with _on(self.device, stream):
-            new = lambda shape: torch.empty(shape, dtype=torch.bfloat16, device=self.device)  # noqa: E731
-            if need_dq:
-                dQ = new(qs) if dQ is None else dQ
-                _want("dQ", dQ, qs, torch.bfloat16, self.device)
+        bf16, dev = torch.bfloat16, self.device
+        _want("Q", Q, qs, bf16, dev)
+        _want("K", K, ks, bf16, dev)
+        _want("V", V, ks, bf16, dev)
+        _want("O", O, qs, bf16, dev)
+        _want("lse", lse, (B, Hq, N), torch.float32, dev)
+        _want("dO", dO, qs, bf16, dev)
+        for label, t, shape in (("dQ", dQ, qs), ("dK", dK, ks), ("dV", dV, ks)):
+            if t is not None:
+                _want(label, t, shape, bf16, dev)
+        if workspace is not None and (workspace.device != dev or not workspace.is_contiguous()):
+            raise ValueError(f"workspace: expected contiguous memory on {dev}")
+        with _on(dev, stream):
+            if need_dq and dQ is None:
+                dQ = torch.empty(qs, dtype=bf16, device=dev)
             if need_dkv:
-                dK, dV = new(ks) if dK is None else dK, new(ks) if dV is None else dV
-                _want("dK", dK, ks, torch.bfloat16, self.device)
-                _want("dV", dV, ks, torch.bfloat16, self.device)
+                dK = torch.empty(ks, dtype=bf16, device=dev) if dK is None else dK
+                dV = torch.empty(ks, dtype=bf16, device=dev) if dV is None else dV
             if workspace is None:
-                workspace = torch.empty(self.attn_bwd_workspace_bytes(), dtype=torch.uint8, device=self.device)
-            elif workspace.device != self.device or not workspace.is_contiguous():
-                raise ValueError(f"workspace: expected contiguous memory on {self.device}")
-            _check(name, call(_ptr(O), _ptr(lse), _ptr(dO), _ptr(dQ), _ptr(dK), _ptr(dV), _ptr(workspace),
-                              workspace.numel() * workspace.element_size(), _stream(stream)))
+                workspace = torch.empty(self._bwd_bytes, dtype=torch.uint8, device=dev)
+            _check(name, call(Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(), lse.data_ptr(), dO.data_ptr(),
+                              _ptr(dQ), _ptr(dK), _ptr(dV), workspace.data_ptr(),
+                              workspace.numel() * workspace.element_size(), _stream_on(dev, stream)))
         return dQ, dK, dV
 
     def dense_attn_bwd(self, Q, K, V, O, lse, dO, dQ=None, dK=None, dV=None, need_dq=True, need_dkv=True,
@@ -395,7 +410,7 @@ class SparsePR:
         one that need_dq / need_dkv leave out). workspace: attn_bwd_workspace_bytes() of device memory that
         a program may keep; None takes it from torch for this call."""
         return self._bwd("sparsepr_dense_attn_bwd",
-                         lambda *a: self.lib.sparsepr_dense_attn_bwd(self.h, _ptr(Q), _ptr(K), _ptr(V), *a),
+                         lambda *a: self.lib.sparsepr_dense_attn_bwd(self.h, *a),
                          Q, K, V, O, lse, dO, dQ, dK, dV, need_dq, need_dkv, workspace, stream)
 
     def blocksparse_attn_bwd(self, Qp, Kp, Vp, part: Partition, route: Route, Osp, lse, dOsp, dQ=None, dK=None,
@@ -405,8 +420,8 @@ class SparsePR:
         and dV in the original token order out. A partition or route whose buffers the handle owns is
         overwritten by the handle's next call: keep copies (partition_views, route_views) across calls."""
         return self._bwd("sparsepr_blocksparse_attn_bwd",
-                         lambda *a: self.lib.sparsepr_blocksparse_attn_bwd(
-                             self.h, _ptr(Qp), _ptr(Kp), _ptr(Vp), ctypes.byref(part), ctypes.byref(route), *a),
+                         lambda q, k, v, *a: self.lib.sparsepr_blocksparse_attn_bwd(
+                             self.h, q, k, v, ctypes.byref(part), ctypes.byref(route), *a),
                          Qp, Kp, Vp, Osp, lse, dOsp, dQ, dK, dV, need_dq, need_dkv, workspace, stream)
 
     # ------------------------------------------------------------------ introspection
@@ -521,8 +536,10 @@ class Rope:
             amplitude = 0.1 * math.log(factor) + 1.0 if scaling == "yarn" else 1.0
         self.amplitude = float(amplitude)
         self.lib = load_library()
-        self._base = RopeConfig(0, 0, 0, d, self.layout, len(widths), 0, (ctypes.c_int * 3)(*widths), 0, 0, 0, 0,
-                                self.amplitude, (ctypes.c_double * 64)(*self.freq))
+        self._plans = {}
+        import torch
+
+        self._int32 = torch.int32
 
     @staticmethod
     def _frequencies(w, base, scaling, factor, trained, beta_fast, beta_slow):
@@ -544,6 +561,20 @@ class Rope:
         return [f / factor * s + f * (1.0 - s) for f, s in zip(freq, slow)]
 
     def _config(self, model, pos):
+        """The call's plan for this shape, strides and type, checked when first met."""
+        key = (model.shape, model.stride(), model.dtype, pos.shape)
+        c = self._plans.get(key)
+        if c is None:
+            c = self._plan(model, pos)
+            if len(self._plans) >= 256:
+                self._plans.clear()
+            self._plans[key] = c
+        if pos.dtype is not self._int32 or pos.device != model.device or not pos.is_contiguous() or not model.is_cuda:
+            raise ValueError(f"positions: expected a contiguous int32 tensor on {model.device} (a CUDA device), got "
+                             f"{pos.dtype} on {pos.device}")
+        return c
+
+    def _plan(self, model, pos):
         import torch
 
         if model.dim() != 4 or model.shape[3] != self.d or model.stride(3) != 1 or 0 in model.shape:
@@ -553,17 +584,12 @@ class Rope:
             raise ValueError(f"token-major tensor of {model.dtype}: bfloat16 or float32")
         B, N, H, d = model.shape
         axes = len(self.widths)
-        if tuple(pos.shape) not in ((N, axes), (B, N, axes)) or pos.dtype != torch.int32 or not pos.is_contiguous() \
-                or pos.device != model.device:
-            raise ValueError(f"positions: expected a contiguous int32 tensor [{N}, {axes}] or [{B}, {N}, {axes}] on "
-                             f"{model.device}, got {pos.dtype} {tuple(pos.shape)} on {pos.device}")
-        if not model.is_cuda:
-            raise ValueError("tensors must be on a CUDA device")
-        c = RopeConfig.from_buffer_copy(self._base)      # one per call: calls of several threads do not meet
-        c.B, c.H, c.N, c.dtype = B, H, N, 1 if model.dtype == torch.float32 else 0
-        c.stride_b, c.stride_n, c.stride_h, _ = model.stride()
-        c.pos_stride_b = N * axes if pos.dim() == 3 else 0
-        return c
+        if tuple(pos.shape) not in ((N, axes), (B, N, axes)):
+            raise ValueError(f"positions: expected [{N}, {axes}] or [{B}, {N}, {axes}], got {tuple(pos.shape)}")
+        c = RopeConfig(B, H, N, d, self.layout, axes, 1 if model.dtype == torch.float32 else 0,
+                       (ctypes.c_int * 3)(*self.widths), *model.stride()[:3], N * axes if pos.dim() == 3 else 0,
+                       self.amplitude, (ctypes.c_double * 64)(*self.freq))
+        return ctypes.byref(c)
 
     def forward(self, x, pos, out=None, stream=None):
         """x [B, N, H, d] bf16 or fp32 (any strides of 16-byte multiples, e.g. a slice of a fused projection)
@@ -571,13 +597,14 @@ class Rope:
         import torch
 
         cfg = self._config(x, pos)
-        shape = (cfg.B, cfg.H, cfg.N, cfg.d)
+        B, N, H, d = x.shape
         with _on(x.device, stream):
             if out is None:
-                out = torch.empty(shape, dtype=torch.bfloat16, device=x.device)
-            _want("out", out, shape, torch.bfloat16, x.device)
-            _check("sparsepr_rope", self.lib.sparsepr_rope(ctypes.byref(cfg), _ptr(x), _ptr(pos), _ptr(out),
-                                                           _stream(stream)))
+                out = torch.empty((B, H, N, d), dtype=torch.bfloat16, device=x.device)
+            else:
+                _want("out", out, (B, H, N, d), torch.bfloat16, x.device)
+            _check("sparsepr_rope", self.lib.sparsepr_rope(cfg, x.data_ptr(), pos.data_ptr(), out.data_ptr(),
+                                                           _stream_on(x.device, stream)))
         return out
 
     def backward(self, dy, pos, out=None, dtype=None, stream=None):
@@ -595,8 +622,8 @@ class Rope:
             elif tuple(out.shape) != (B, N, H, d) or out.device != dy.device:
                 raise ValueError(f"out: expected [{B}, {N}, {H}, {d}] on {dy.device}, got {tuple(out.shape)} on {out.device}")
             cfg = self._config(out, pos)
-            _check("sparsepr_rope_bwd", self.lib.sparsepr_rope_bwd(ctypes.byref(cfg), _ptr(dy), _ptr(pos), _ptr(out),
-                                                                   _stream(stream)))
+            _check("sparsepr_rope_bwd", self.lib.sparsepr_rope_bwd(cfg, dy.data_ptr(), pos.data_ptr(), out.data_ptr(),
+                                                                   _stream_on(dy.device, stream)))
         return out
 
 
