@@ -31,7 +31,14 @@ struct BwdParams {
     int kcap, qcap;                         // list entries per group
     int* status;
     int N, g, Gq, Gk;
+    int kv_tiles, q_tiles;                  // most key tiles of a KV head, query tiles of a query head
+    int kv_blocks;                          // CTAs of dK and dV, before those of dQ
     float scale, scale_log2;
+};
+
+// Tensor maps of [rows][64] boxes of 128 rows.
+struct BwdMaps {
+    CUtensorMap q, k, v, o;
 };
 
 // ---------------------------------------------------------------- per-row terms
@@ -182,16 +189,18 @@ __global__ void __launch_bounds__(256) bwd_lists_kernel(const int32_t* __restric
 // ---------------------------------------------------------------- gradients
 // Both kernels run ten warps: two warpgroups that form P and dS (thread r of warpgroup w owns TMEM
 // lane r of columns 64 w .. 64 w + 63), warp 8 loads tiles (TMA), warp 9 allocates TMEM and issues
-// every MMA. P and dS go back to TMEM as bf16 pairs over the fp32 columns they were formed from
-// (warpgroup w at column 64 w) and are the A operands of the next product, so no transposed copy is
-// ever made: the dK/dV kernel keeps keys in the lanes (S^T = K Q^T), the dQ kernel queries.
+// every MMA. P and dS go back to TMEM as bf16 pairs, where they are the A operands of the next
+// product, so no transposed copy is ever made: the dK/dV kernel keeps keys in the lanes
+// (S^T = K Q^T), the dQ kernel queries. They have columns of their own, so the fp32 columns of S and
+// dP are free again as soon as they have been read, and the next product into them runs beside the
+// arithmetic on the last.
 // Rows of a streamed tile past its valid ones belong to another group or head: the loading warp
 // zeroes them in shared memory, so that no value there, finite or not, reaches a sum.
 constexpr int kRegion = 16384;              // one [128 rows][64 bf16] region, 128-byte swizzle
 constexpr int kThreads = 320;
 constexpr uint32_t kTmemCols = 512;
 
-// Set-up shared by the kernels: aligned shared memory, barriers, TMEM.
+// Set-up shared by the kernels: aligned shared memory, barriers (`count` arrivals each), TMEM.
 struct Cta {
     uint32_t base, bars, tmem;
     unsigned char* sbase;
@@ -200,7 +209,8 @@ struct Cta {
     __device__ __forceinline__ uint32_t bar(int i) const { return bars + 8u * (uint32_t)i; }
 };
 
-__device__ __forceinline__ Cta cta_setup(unsigned char* smem_raw, int off_bar, const int* counts, int nbars) {
+template <typename Count>
+__device__ __forceinline__ Cta cta_setup(unsigned char* smem_raw, int off_bar, int nbars, Count count) {
     Cta c;
     const uint32_t raw = tc::smem_addr(smem_raw);
     c.base = (raw + 1023u) & ~1023u;
@@ -211,7 +221,7 @@ __device__ __forceinline__ Cta cta_setup(unsigned char* smem_raw, int off_bar, c
     uint32_t* slot = reinterpret_cast<uint32_t*>(c.sbase + off_bar + 8 * nbars);
     c.abort_flag = reinterpret_cast<volatile int*>(slot + 1);
     if (threadIdx.x == 0) {
-        for (int i = 0; i < nbars; ++i) tc::mbar_init(c.bar(i), counts[i]);
+        for (int i = 0; i < nbars; ++i) tc::mbar_init(c.bar(i), count(i));
         *c.abort_flag = 0;
         tc::fence_mbar_init();
     }
@@ -239,25 +249,42 @@ __device__ __forceinline__ void cta_finish(const Cta& c, int* status) {
 
 // D[tmem] = A B^T over D columns of two swizzled tiles (both K-major).
 template <int D>
-__device__ __forceinline__ void mma_rows(uint32_t d_tmem, uint32_t a, uint32_t b) {
+__device__ __forceinline__ void mma_rows(uint32_t d_tmem, uint32_t a, uint32_t b, uint32_t go) {
     constexpr uint32_t id = tc::idesc_bf16_f32(kTile, kTile, 0);
+    const uint64_t da = tc::smem_desc_sw128(a, 16, 1024), db = tc::smem_desc_sw128(b, 16, 1024);
 #pragma unroll
     for (int k = 0; k < D / 16; ++k) {
-        const uint32_t off = (uint32_t)((k >> 2) * kRegion + (k & 3) * 32);
-        tc::mma_f16_ss(d_tmem, tc::smem_desc_sw128(a + off, 16, 1024), tc::smem_desc_sw128(b + off, 16, 1024), id,
-                       k > 0 ? 1u : 0u);
+        const uint32_t off = (uint32_t)((k >> 2) * kRegion + (k & 3) * 32) >> 4;     // address field of the descriptors
+        tc::mma_f16_ss_go(d_tmem, da + off, db + off, id, k > 0 ? 1u : 0u, go);
     }
 }
 
-// D[tmem] (+)= A B over the 128 rows of tile b (MN-major); A is bf16 pairs in TMEM, its columns
-// 64..127 packed from column a_tmem + 64.
+// D[tmem] (+)= A B over the 128 rows of tile b (MN-major); A is bf16 pairs in 64 TMEM columns.
 template <int D>
-__device__ __forceinline__ void mma_sums(uint32_t d_tmem, uint32_t a_tmem, uint32_t b, bool accumulate) {
+__device__ __forceinline__ void mma_sums(uint32_t d_tmem, uint32_t a_tmem, uint32_t b, bool accumulate, uint32_t go) {
     constexpr uint32_t id = tc::idesc_bf16_f32(kTile, D, 1);
+    const uint64_t db = tc::smem_desc_sw128(b, kRegion, 1024);
 #pragma unroll
     for (int k = 0; k < kTile / 16; ++k)
-        tc::mma_f16_ts(d_tmem, a_tmem + (uint32_t)(64 * (k >> 2) + 8 * (k & 3)),
-                       tc::smem_desc_sw128(b + (uint32_t)(k * 2048), kRegion, 1024), id, (accumulate || k > 0) ? 1u : 0u);
+        tc::mma_f16_ts_go(d_tmem, a_tmem + (uint32_t)(8 * k), db + (uint64_t)(k * 2048 >> 4), id,
+                          (accumulate || k > 0) ? 1u : 0u, go);
+}
+
+// D[tmem] += A B^T over one K step of 16: [128][16] tiles without swizzle, as two halves of 8 columns.
+constexpr int kExtBytes = 2 * kTile * 16;
+__device__ __forceinline__ void mma_ext(uint32_t d_tmem, uint32_t a, uint32_t b, uint32_t go) {
+    constexpr uint32_t id = tc::idesc_bf16_f32(kTile, kTile, 0);
+    tc::mma_f16_ss_go(d_tmem, tc::smem_desc_none(a, kTile * 16, 128), tc::smem_desc_none(b, kTile * 16, 128), id, 1u, go);
+}
+
+// x as three bf16 parts, x = a + b + c to 24 bits; the packed pairs (a, b) and (c, 0).
+__device__ __forceinline__ void split3(float x, uint16_t (&o)[3]) {
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        const bf16 h = __float2bfloat16_rn(x);
+        o[i] = __bfloat16_as_ushort(h);
+        x -= bf16_to_f32(h);
+    }
 }
 
 template <int D>
@@ -327,6 +354,43 @@ __device__ __forceinline__ uint32_t bf16x2(float a, float b) {
     return *reinterpret_cast<uint32_t*>(&v);
 }
 
+// 2^x of a pair on the FMA pipe: x = n + f with n the nearest integer (by adding 1.5 2^23) and |f| <= 1/2,
+// 2^f by a least-maximum polynomial of degree 4 (relative error 2.7e-6, 2^-18.5, fitted here), 2^n by
+// adding n to the exponent. Exponents below -126 give 2^-126.
+__device__ __forceinline__ uint64_t ex2_fma(uint64_t x2) {
+    float a, b;
+    up2(x2, a, b);
+    const uint64_t x = pk2(fmaxf(a, -126.f), fmaxf(b, -126.f));
+    const uint64_t t = add2(x, pk2(12582912.f, 12582912.f));
+    const uint64_t f = fma2(add2(t, pk2(-12582912.f, -12582912.f)), pk2(-1.f, -1.f), x);
+    uint64_t q = pk2(0.009570096619427204f, 0.009570096619427204f);
+    q = fma2(q, f, pk2(0.05591785907745361f, 0.05591785907745361f));
+    q = fma2(q, f, pk2(0.240247443318367f, 0.240247443318367f));
+    q = fma2(q, f, pk2(0.6931217908859253f, 0.6931217908859253f));
+    q = fma2(q, f, pk2(0.9999992847442627f, 0.9999992847442627f));
+    float q0, q1, t0, t1;
+    up2(q, q0, q1);
+    up2(t, t0, t1);
+    return pk2(__int_as_float(__float_as_int(q0) + (__float_as_int(t0) << 23)),
+               __int_as_float(__float_as_int(q1) + (__float_as_int(t1) << 23)));
+}
+
+// 2^x of pair i of a row. The special-function unit alone would take 1024 cycles a 128 x 128 tile,
+// most of the arithmetic's time; three pairs of eight go to the FMA pipe instead (12 heads x 4096 rows,
+// d = 128, both passes: 297 us with none, 290, 282, 281.5 and 287 us with one to four).
+__device__ __forceinline__ void ex2_pair(uint64_t x2, int i, uint32_t& a, uint32_t& b) {
+    float x0, x1;
+    if (i % 8 < 3) {
+        up2(ex2_fma(x2), x0, x1);
+    } else {
+        up2(x2, x0, x1);
+        x0 = ex2(x0);
+        x1 = ex2(x1);
+    }
+    a = __float_as_uint(x0);
+    b = __float_as_uint(x1);
+}
+
 // One fp32 accumulator row of D TMEM columns, times `scale`, rounded to bf16 into `out`.
 template <int D>
 __device__ __forceinline__ void store_acc_row(uint32_t tacc, float scale, bf16* out, bool zero) {
@@ -383,166 +447,167 @@ __device__ __forceinline__ bool find_tile(const int32_t* off, const int32_t* til
 // ---------------------------------------------------------------- dK and dV
 // One CTA per 128-key tile, streaming the (Q, dO) tiles of every query head of the KV head and
 // every query tile that keeps the key group. Per tile, with keys in the TMEM lanes:
-//   S^T = K Q^T -> P^T (over S^T);  dV += P^T dO;  dP^T = V dO^T -> dS^T (over dP^T);  dK += dS^T Q.
-// Issue order dV(i), S(i+1), dK(i), dP(i+1): the exponentials of tile i + 1 run beside dK(i) and
-// dP(i+1), dS(i) beside dV(i) and S(i+1).
+//   S^T = K Q^T -> P^T;  dV += P^T dO;  dP^T = V dO^T -> dS^T;  dK += dS^T Q.
+// dV and dK take 256 of the 512 TMEM columns, P and dS 64 each; S and dP share the other 128 in
+// turn: dP(i) is issued when S(i) has been read, S(i+1) when dP(i) has. Issue order dP(i),
+// dK(i-1), S(i+1), dV(i): dP and dK run beside the exponentials, S and dV beside dS.
+// The terms -lse and -D of a query vary along the columns here, so a thread would need every query's:
+// they are added by the products instead. One more K step of 16 multiplies ones on the key side with
+// the three bf16 parts (24 bits) of -lse sqrt(d), or of -D, on the query side.
+// Four 128-row buffers hold the streamed tiles. dO(i) is done with a product before Q(i), and Q(i+2)
+// is wanted before dO(i+2): Q(i+2) takes the buffer of dO(i), dO(i+2) that of Q(i).
 namespace kv {
 constexpr int kStages = 2;
-constexpr int kOffK = 0, kOffV = 2 * kRegion, kOffQ = 4 * kRegion, kOffO = kOffQ + kStages * 2 * kRegion,
-              kOffRows = kOffO + kStages * 2 * kRegion;         // per warp: 2 buffers of 64 -lse and 64 -D
-constexpr int kOffBar = kOffRows + 8 * 2 * 128 * 4;
-enum { kKV = 0, kQf = 1, kOf = kQf + kStages, kQe = kOf + kStages, kOe = kQe + kStages, kS = kOe + kStages, kP = kS + 1,
-       kDP = kP + 1, kDS = kDP + 1, kDone = kDS + 1, kLand = kDone + 1, kBars = kLand + 1 };
+constexpr int kOffK = 0, kOffV = 2 * kRegion, kOffBuf = 4 * kRegion, kOffExt = kOffBuf + 2 * kStages * 2 * kRegion,
+              kOffOne = kOffExt + kStages * kExtBytes, kOffBar = kOffOne + 2 * kExtBytes;
+// Buffers of tile i: stage i % 2 has two, which Q and dO swap from one use of the stage to the next.
+__device__ __forceinline__ int buf_q(int i) { return kOffBuf + (2 * (i & 1) + ((i >> 1) & 1)) * 2 * kRegion; }
+__device__ __forceinline__ int buf_o(int i) { return kOffBuf + (2 * (i & 1) + (((i >> 1) & 1) ^ 1)) * 2 * kRegion; }
+// full / empty stages (Q's full one also stands for the row terms); S and dP ready, read; P and dS written;
+// all MMAs done; ragged loads
+enum { kKV = 0, kQf = 1, kOf = kQf + kStages, kQe = kOf + kStages, kOe = kQe + kStages, kS = kOe + kStages, kDP, kDone, kLand,
+       kSread, kDPread, kP, kDS, kBars };
 constexpr int kSmem = kOffBar + 8 * kBars + 16 + 1024;
 static_assert(kSmem <= 232448, "shared memory budget");
-constexpr uint32_t kTS = 0, kTDP = 128, kTDV = 256, kTDK = 384;
+constexpr uint32_t kTS = 0, kTP = 128, kTDS = 192, kTDV = 256, kTDK = 384;      // dP: the columns of S
 }  // namespace kv
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1) bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmQ,
-                                                              const __grid_constant__ CUtensorMap tmK,
-                                                              const __grid_constant__ CUtensorMap tmV,
-                                                              const __grid_constant__ CUtensorMap tmO,
-                                                              const BwdParams p) {
+__device__ __forceinline__ void dkv_tile(const BwdMaps& m, const BwdParams& p, unsigned char* smem_raw, int z, int pair) {
     using namespace kv;
-    extern __shared__ unsigned char smem_raw[];
-    if (p.status && *reinterpret_cast<volatile int*>(p.status) == kDevTimeout) return;
-    const int z = blockIdx.y;
     int grp, klo, kn;
-    if (!find_tile(p.koff, p.ktile_off, z, p.Gk, p.N, blockIdx.x, grp, klo, kn)) return;
+    if (!find_tile(p.koff, p.ktile_off, z, p.Gk, p.N, pair, grp, klo, kn)) return;
     const int2* list = p.qlist + ((long long)z * p.Gk + grp) * p.qcap;
     const int nt = p.qcnt ? p.qcnt[(long long)z * p.Gk + grp] : (p.N + kTile - 1) / kTile;
     const int iters = nt * p.g;
-    // tile `it`: head, first row and valid rows
     auto tile = [&](int t) { return p.qcnt ? list[t] : make_int2(t * kTile, min(kTile, p.N - t * kTile)); };
-    const int counts[kBars] = {1, 1, 1, 1, 1, 1, 1, 1, 1, 1, 256, 1, 256, 1, 1};
-    const Cta c = cta_setup(smem_raw, kOffBar, counts, kBars);
+    {
+        // ones under the parts of -lse (columns 0-2), or under those of -D (3-5); the halves of columns
+        // 8-15 are zero everywhere
+        const uint32_t off = ((tc::smem_addr(smem_raw) + 1023u) & ~1023u) - tc::smem_addr(smem_raw);
+        uint4* ext = reinterpret_cast<uint4*>(smem_raw + off + kOffExt);
+        constexpr uint32_t one = 0x3f80u;
+        for (int i = threadIdx.x; i < (kStages + 2) * 2 * kTile; i += kThreads) {
+            const int t = i / (2 * kTile);
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (i % (2 * kTile) < kTile && t == kStages) v = make_uint4(one | one << 16, one, 0, 0);
+            if (i % (2 * kTile) < kTile && t == kStages + 1) v = make_uint4(0, one << 16, one | one << 16, 0);
+            ext[i] = v;
+        }
+        tc::fence_proxy_async_smem();
+    }
+    const Cta c = cta_setup(smem_raw, kOffBar, kBars, [](int i) { return i >= kSread ? 256 : i >= kQf && i < kOf ? 2 : 1; });
 
     if (c.warp == 8) {
         if (c.lane == 0) {
             tc::mbar_arrive_expect_tx(c.bar(kKV), 2 * (D / 64) * kRegion);
             for (int h = 0; h < D / 64; ++h) {
-                tc::tma_load_2d(c.base + kOffK + h * kRegion, &tmK, c.bar(kKV), 64 * h, z * p.N + klo);
-                tc::tma_load_2d(c.base + kOffV + h * kRegion, &tmV, c.bar(kKV), 64 * h, z * p.N + klo);
+                tc::tma_load_2d(c.base + kOffK + h * kRegion, &m.k, c.bar(kKV), 64 * h, z * p.N + klo);
+                tc::tma_load_2d(c.base + kOffV + h * kRegion, &m.v, c.bar(kKV), 64 * h, z * p.N + klo);
             }
         }
         __syncwarp();
         int nland = 0, nq = 0, no = 0, t = 0, x = z * p.g;
+        // this lane's four rows of the next tile's terms; rows past its end give P = 2^(-huge) = 0
+        float nl[4], nd[4];
+        auto fetch = [&](int2 e, int head) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int r = 32 * j + c.lane;
+                const long long at = (long long)head * p.N + e.x + r;
+                nl[j] = r < e.y ? __ldg(p.nlse2 + at) : -INFINITY;
+                nd[j] = r < e.y ? __ldg(p.nD + at) : 0.f;
+            }
+        };
+        const float inv = 1.f / p.scale_log2;
+        int2 e = iters > 0 ? tile(0) : make_int2(0, 0);
+        if (iters > 0) fetch(e, x);
         for (int it = 0; it < iters; ++it) {
-            const int2 e = tile(t);
-            const int s = it % kStages, row = x * p.N + e.x;
-            if (it >= kStages && !__all_sync(kFull, tc::mbar_wait(c.bar(kQe + s), (it / kStages - 1) & 1, c.abort_flag))) break;
-            if (!load_tile_zeroed<D>(c, c.base + kOffQ + s * 2 * kRegion, &tmQ, kQf + s, kLand, nland, row, e.y)) break;
-            nq = it + 1;
-            if (it >= kStages && !__all_sync(kFull, tc::mbar_wait(c.bar(kOe + s), (it / kStages - 1) & 1, c.abort_flag))) break;
-            if (!load_tile_zeroed<D>(c, c.base + kOffO + s * 2 * kRegion, &tmO, kOf + s, kLand, nland, row, e.y)) break;
-            no = it + 1;
+            const int s = it % kStages, row = x * p.N + e.x, valid = e.y;
             if (++t == nt) {
                 t = 0;
                 ++x;
             }
+            const int2 next = it + 1 < iters ? tile(t) : make_int2(0, 0);
+            // Q(it) follows dO(it - 2) in its buffer, dO(it) follows Q(it - 2)
+            if (it >= kStages && !__all_sync(kFull, tc::mbar_wait(c.bar(kOe + s), (it / kStages - 1) & 1, c.abort_flag))) break;
+            if (!load_tile_zeroed<D>(c, c.base + buf_q(it), &m.q, kQf + s, kLand, nland, row, valid)) break;
+            nq = it + 1;
+            uint4* ext = reinterpret_cast<uint4*>(c.sbase + kOffExt + s * kExtBytes);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint16_t a[3], b[3];
+                split3(fmaxf(nl[j] * inv, -1e30f), a);
+                split3(nd[j], b);
+                if (isnan(nl[j])) a[0] = 0x7fffu;       // fmaxf drops NaN
+                ext[32 * j + c.lane] = make_uint4(a[0] | (uint32_t)a[1] << 16, a[2] | (uint32_t)b[0] << 16,
+                                                  b[1] | (uint32_t)b[2] << 16, 0);
+            }
+            tc::fence_proxy_async_smem();
+            __syncwarp();
+            if (c.lane == 0) tc::mbar_arrive(c.bar(kQf + s));
+            if (it + 1 < iters) fetch(next, x);
+            if (it >= kStages && !__all_sync(kFull, tc::mbar_wait(c.bar(kQe + s), (it / kStages - 1) & 1, c.abort_flag))) break;
+            if (!load_tile_zeroed<D>(c, c.base + buf_o(it), &m.o, kOf + s, kLand, nland, row, valid)) break;
+            no = it + 1;
+            e = next;
         }
         // every issued load lands before the CTA can exit
         int never = 0;
-        for (int m = max(0, nq - kStages); m < nq; ++m) tc::mbar_wait(c.bar(kQf + m % kStages), (m / kStages) & 1, &never);
-        for (int m = max(0, no - kStages); m < no; ++m) tc::mbar_wait(c.bar(kOf + m % kStages), (m / kStages) & 1, &never);
+        for (int i = max(0, nq - kStages); i < nq; ++i) tc::mbar_wait(c.bar(kQf + i % kStages), (i / kStages) & 1, &never);
+        for (int i = max(0, no - kStages); i < no; ++i) tc::mbar_wait(c.bar(kOf + i % kStages), (i / kStages) & 1, &never);
         tc::mbar_wait(c.bar(kKV), 0, &never);
     } else if (c.warp == 9) {
+        const uint32_t go = tc::elect_one();
         auto wait = [&](int b, int parity) {
             const bool ok = __all_sync(kFull, tc::mbar_wait(c.bar(b), parity & 1, c.abort_flag));
             tc::fence_after_sync();
             return ok;
         };
-        const uint32_t tS = c.tmem + kTS, tDP = c.tmem + kTDP;
-        auto q = [&](int it) { return c.base + kOffQ + (it % kStages) * 2 * kRegion; };
-        auto o = [&](int it) { return c.base + kOffO + (it % kStages) * 2 * kRegion; };
+        const uint32_t tS = c.tmem + kTS;
+        auto q = [&](int it) { return c.base + buf_q(it); };
+        auto o = [&](int it) { return c.base + buf_o(it); };
+        auto ext = [&](int it) { return c.base + kOffExt + (it % kStages) * kExtBytes; };
+        auto issue_S = [&](int it) {
+            mma_rows<D>(tS, c.base + kOffK, q(it), go);
+            mma_ext(tS, c.base + kOffOne, ext(it), go);
+            tc::commit_go(c.bar(kS), go);
+        };
+        auto issue_dK = [&](int it) {
+            if (!wait(kDS, it)) return false;
+            mma_sums<D>(c.tmem + kTDK, c.tmem + kTDS, q(it), it > 0, go);
+            tc::commit_go(c.bar(kQe + it % kStages), go);
+            return true;
+        };
         bool ok = iters > 0 && wait(kKV, 0) && wait(kQf, 0);
-        if (ok) {
-            if (c.lane == 0) {
-                mma_rows<D>(tS, c.base + kOffK, q(0));
-                tc::commit(c.bar(kS));
-            }
-            __syncwarp();
-            ok = wait(kOf, 0);
-        }
-        if (ok) {
-            if (c.lane == 0) {
-                mma_rows<D>(tDP, c.base + kOffV, o(0));
-                tc::commit(c.bar(kDP));
-            }
-            __syncwarp();
-        }
+        if (ok) issue_S(0);
         for (int it = 0; ok && it < iters; ++it) {
-            const bool more = it + 1 < iters;
-            if (more && !wait(kQf + (it + 1) % kStages, (it + 1) / kStages)) break;
+            if (!wait(kOf + it % kStages, it / kStages) || !wait(kSread, it)) break;
+            mma_rows<D>(tS, c.base + kOffV, o(it), go);
+            mma_ext(tS, c.base + kOffOne + kExtBytes, ext(it), go);
+            tc::commit_go(c.bar(kDP), go);
+            if (it > 0 && !issue_dK(it - 1)) break;
+            if (it + 1 < iters) {
+                if (!wait(kQf + (it + 1) % kStages, (it + 1) / kStages) || !wait(kDPread, it)) break;
+                issue_S(it + 1);
+            }
             if (!wait(kP, it)) break;
-            if (c.lane == 0) {
-                mma_sums<D>(c.tmem + kTDV, tS, o(it), it > 0);
-                tc::commit(c.bar(kOe + it % kStages));
-                if (more) {
-                    mma_rows<D>(tS, c.base + kOffK, q(it + 1));
-                    tc::commit(c.bar(kS));
-                }
-            }
-            __syncwarp();
-            if (more && !wait(kOf + (it + 1) % kStages, (it + 1) / kStages)) break;
-            if (!wait(kDS, it)) break;
-            if (c.lane == 0) {
-                mma_sums<D>(c.tmem + kTDK, tDP, q(it), it > 0);
-                tc::commit(c.bar(kQe + it % kStages));
-                if (more) {
-                    mma_rows<D>(tDP, c.base + kOffV, o(it + 1));
-                    tc::commit(c.bar(kDP));
-                }
-            }
-            __syncwarp();
+            mma_sums<D>(c.tmem + kTDV, c.tmem + kTP, o(it), it > 0, go);
+            tc::commit_go(c.bar(kOe + it % kStages), go);
+            if (it + 1 == iters) issue_dK(it);
         }
         // every issued MMA completes before the sums are read and TMEM is released
-        if (c.lane == 0) tc::commit(c.bar(kDone));
-        __syncwarp();
+        tc::commit_go(c.bar(kDone), go);
         int never = 0;
         tc::mbar_wait(c.bar(kDone), 0, &never);
     } else {
         const int w = c.warp >> 2, r = threadIdx.x & 127;
         const uint32_t lane_off = (uint32_t)((c.warp & 3) * 32) << 16;
-        const uint32_t tS = c.tmem + kTS + 64 * w + lane_off, tDP = c.tmem + kTDP + 64 * w + lane_off;
-        float* buf = reinterpret_cast<float*>(c.sbase + kOffRows) + c.warp * 256;
+        const uint32_t tS = c.tmem + kTS + 64 * w + lane_off;
+        const uint32_t tP = c.tmem + kTP + 32 * w + lane_off, tDS = c.tmem + kTDS + 32 * w + lane_off;
         const uint64_t cc = pk2(p.scale_log2, p.scale_log2);
-        // this lane's two columns of -lse log2(e) and -D of a tile; rows past its end give P = 0
-        float nl[2], nd[2];
-        auto fetch = [&](int2 e, int x) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int col = 64 * w + 32 * i + c.lane;
-                const long long at = (long long)x * p.N + e.x + col;
-                nl[i] = col < e.y ? __ldg(p.nlse2 + at) : -INFINITY;
-                nd[i] = col < e.y ? __ldg(p.nD + at) : 0.f;
-            }
-        };
-        int t = 0, x = z * p.g;
-        auto advance = [&]() {
-            if (++t == nt) {
-                t = 0;
-                ++x;
-            }
-        };
-        if (iters > 0) fetch(tile(0), x);
-        advance();
-        int2 next = iters > 1 ? tile(t) : make_int2(0, 0);
         bool ok = true;
         for (int it = 0; it < iters; ++it) {
-            float* row = buf + (it & 1) * 128;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                row[32 * i + c.lane] = nl[i];
-                row[64 + 32 * i + c.lane] = nd[i];
-            }
-            __syncwarp();
-            if (it + 1 < iters) {
-                fetch(next, x);
-                advance();
-                if (it + 2 < iters) next = tile(t);
-            }
             if (!__all_sync(kFull, tc::mbar_wait(c.bar(kS), it & 1, c.abort_flag))) { ok = false; break; }
             tc::fence_after_sync();
             uint32_t pv[2][32];
@@ -551,55 +616,52 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_dkv_kernel(const __grid_const
             tc::tmem_wait_ld();
             tc::regs_after_wait(pv[0]);
             tc::regs_after_wait(pv[1]);
+            tc::fence_before_sync();
+            tc::mbar_arrive(c.bar(kSread));
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int i = 0; i < 32; i += 2)
+                    ex2_pair(mul2(pk2(__uint_as_float(pv[h][i]), __uint_as_float(pv[h][i + 1])), cc), i / 2, pv[h][i],
+                             pv[h][i + 1]);
+            // P(it) and dS(it) follow P(it - 1) and dS(it - 1) once dV and dK have taken those in
+            const int prev = (it - 1) % kStages, phase = ((it - 1) / kStages) & 1;
+            if (it > 0 && !__all_sync(kFull, tc::mbar_wait(c.bar(kOe + prev), phase, c.abort_flag))) { ok = false; break; }
+            tc::fence_after_sync();
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 uint32_t pk[16];
 #pragma unroll
-                for (int e = 0; e < 16; e += 2) {
-                    const float4 l4 = *reinterpret_cast<const float4*>(row + 32 * h + 2 * e);
-                    const float ls[4] = {l4.x, l4.y, l4.z, l4.w};
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const int i = 2 * (e + u);
-                        float x0, x1;
-                        up2(fma2(pk2(__uint_as_float(pv[h][i]), __uint_as_float(pv[h][i + 1])), cc, pk2(ls[2 * u], ls[2 * u + 1])),
-                            x0, x1);
-                        x0 = ex2(x0);
-                        x1 = ex2(x1);
-                        pk[e + u] = bf16x2(x0, x1);
-                        pv[h][i] = __float_as_uint(x0);
-                        pv[h][i + 1] = __float_as_uint(x1);
-                    }
-                }
-                tc::tmem_st16(tS + 16 * h, pk);
+                for (int e = 0; e < 16; ++e) pk[e] = bf16x2(__uint_as_float(pv[h][2 * e]), __uint_as_float(pv[h][2 * e + 1]));
+                tc::tmem_st16(tP + 16 * h, pk);
             }
             tc::tmem_wait_st();
             tc::fence_before_sync();
             tc::mbar_arrive(c.bar(kP));
             if (!__all_sync(kFull, tc::mbar_wait(c.bar(kDP), it & 1, c.abort_flag))) { ok = false; break; }
             tc::fence_after_sync();
+            uint32_t dv[2][32];
+            tc::tmem_ld32(tS, dv[0]);
+            tc::tmem_ld32(tS + 32, dv[1]);
+            tc::tmem_wait_ld();
+            tc::regs_after_wait(dv[0]);
+            tc::regs_after_wait(dv[1]);
+            tc::fence_before_sync();
+            tc::mbar_arrive(c.bar(kDPread));
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                uint32_t dv[32], pk[16];
-                tc::tmem_ld32(tDP + 32 * h, dv);
-                tc::tmem_wait_ld();
-                tc::regs_after_wait(dv);
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
-                for (int e = 0; e < 16; e += 2) {
-                    const float4 d4 = *reinterpret_cast<const float4*>(row + 64 + 32 * h + 2 * e);
-                    const float ds[4] = {d4.x, d4.y, d4.z, d4.w};
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const int i = 2 * (e + u);
-                        float x0, x1;
-                        up2(mul2(add2(pk2(__uint_as_float(dv[i]), __uint_as_float(dv[i + 1])), pk2(ds[2 * u], ds[2 * u + 1])),
-                                 pk2(__uint_as_float(pv[h][i]), __uint_as_float(pv[h][i + 1]))),
-                            x0, x1);
-                        pk[e + u] = bf16x2(x0, x1);
-                    }
+                for (int e = 0; e < 16; ++e) {
+                    float x0, x1;
+                    up2(mul2(pk2(__uint_as_float(dv[h][2 * e]), __uint_as_float(dv[h][2 * e + 1])),
+                             pk2(__uint_as_float(pv[h][2 * e]), __uint_as_float(pv[h][2 * e + 1]))),
+                        x0, x1);
+                    pv[h][e] = bf16x2(x0, x1);      // over columns that have been used
                 }
-                tc::tmem_st16(tDP + 16 * h, pk);
-            }
+            if (it > 0 && !__all_sync(kFull, tc::mbar_wait(c.bar(kQe + prev), phase, c.abort_flag))) { ok = false; break; }
+            tc::fence_after_sync();
+            tc::tmem_st16(tDS, pv[0]);
+            tc::tmem_st16(tDS + 16, pv[1]);
             tc::tmem_wait_st();
             tc::fence_before_sync();
             tc::mbar_arrive(c.bar(kDS));
@@ -616,43 +678,36 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_dkv_kernel(const __grid_const
 
 // ---------------------------------------------------------------- dQ
 // One CTA per 128-query tile of a query head, streaming the (K, V) tiles of its kept keys. Per
-// tile, with queries in the TMEM lanes: S = Q K^T -> P;  dP = dO V^T;  dS (over S);  dQ += dS K.
-// S has two buffers, so S(j+1) is ready when the warpgroups turn to it; dP(j+1) is issued as soon
-// as dP(j) has been read.
+// tile, with queries in the TMEM lanes: S = Q K^T -> P;  dP = dO V^T -> dS;  dQ += dS K. S(j+1) is
+// issued as soon as S(j) has been read, dP(j+1) as soon as dP(j) has.
 namespace dq {
 constexpr int kKStages = 3, kVStages = 2;
 constexpr int kOffQ = 0, kOffO = 2 * kRegion, kOffK = 4 * kRegion, kOffV = kOffK + kKStages * 2 * kRegion,
               kOffBar = kOffV + kVStages * 2 * kRegion;
-enum { kQO = 0, kKf = 1, kVf = kKf + kKStages, kKe = kVf + kVStages, kVe = kKe + kKStages, kS = kVe + kVStages, kDP = kS + 2,
-       kRead = kDP + 1, kDS = kRead + 1, kDone = kDS + 1, kLand = kDone + 1, kBars = kLand + 1 };
+enum { kQO = 0, kKf = 1, kVf = kKf + kKStages, kKe = kVf + kVStages, kVe = kKe + kKStages, kS = kVe + kVStages, kDP, kDSfree,
+       kDone, kLand, kSread, kDPread, kDS, kBars };
 constexpr int kSmem = kOffBar + 8 * kBars + 16 + 1024;
 static_assert(kSmem <= 232448, "shared memory budget");
-constexpr uint32_t kTS = 0, kTDP = 256, kTDQ = 384;
+constexpr uint32_t kTS = 0, kTDP = 128, kTDQ = 256, kTDS = 384;
 }  // namespace dq
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1) bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ,
-                                                             const __grid_constant__ CUtensorMap tmK,
-                                                             const __grid_constant__ CUtensorMap tmV,
-                                                             const __grid_constant__ CUtensorMap tmO, const BwdParams p) {
+__device__ __forceinline__ void dq_tile(const BwdMaps& m, const BwdParams& p, unsigned char* smem_raw, int x, int pair) {
     using namespace dq;
-    extern __shared__ unsigned char smem_raw[];
-    if (p.status && *reinterpret_cast<volatile int*>(p.status) == kDevTimeout) return;
-    const int x = blockIdx.y, z = x / p.g;
+    const int z = x / p.g;
     int grp, qlo, qn;
-    if (!find_tile(p.qoff, p.qtile_off, z, p.Gq, p.N, blockIdx.x, grp, qlo, qn)) return;
+    if (!find_tile(p.qoff, p.qtile_off, z, p.Gq, p.N, pair, grp, qlo, qn)) return;
     const int2* list = p.klist + ((long long)z * p.Gq + grp) * p.kcap;
     const int nt = p.kcnt ? p.kcnt[(long long)z * p.Gq + grp] : (p.N + kTile - 1) / kTile;
     auto tile = [&](int t) { return p.kcnt ? list[t] : make_int2(t * kTile, min(kTile, p.N - t * kTile)); };
-    const int counts[kBars] = {1, 1, 1, 1, 1, 1, 1, 1, 1, 1, 1, 1, 1, 1, 256, 256, 1, 1};
-    const Cta c = cta_setup(smem_raw, kOffBar, counts, kBars);
+    const Cta c = cta_setup(smem_raw, kOffBar, kBars, [](int i) { return i >= kSread ? 256 : 1; });
 
     if (c.warp == 8) {
         if (c.lane == 0) {
             tc::mbar_arrive_expect_tx(c.bar(kQO), 2 * (D / 64) * kRegion);
             for (int h = 0; h < D / 64; ++h) {
-                tc::tma_load_2d(c.base + kOffQ + h * kRegion, &tmQ, c.bar(kQO), 64 * h, x * p.N + qlo);
-                tc::tma_load_2d(c.base + kOffO + h * kRegion, &tmO, c.bar(kQO), 64 * h, x * p.N + qlo);
+                tc::tma_load_2d(c.base + kOffQ + h * kRegion, &m.q, c.bar(kQO), 64 * h, x * p.N + qlo);
+                tc::tma_load_2d(c.base + kOffO + h * kRegion, &m.o, c.bar(kQO), 64 * h, x * p.N + qlo);
             }
         }
         __syncwarp();
@@ -661,17 +716,18 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_dq_kernel(const __grid_consta
             const int2 e = tile(t);
             const int sk = t % kKStages, sv = t % kVStages, row = z * p.N + e.x;
             if (t >= kKStages && !__all_sync(kFull, tc::mbar_wait(c.bar(kKe + sk), (t / kKStages - 1) & 1, c.abort_flag))) break;
-            if (!load_tile_zeroed<D>(c, c.base + kOffK + sk * 2 * kRegion, &tmK, kKf + sk, kLand, nland, row, e.y)) break;
+            if (!load_tile_zeroed<D>(c, c.base + kOffK + sk * 2 * kRegion, &m.k, kKf + sk, kLand, nland, row, e.y)) break;
             nk = t + 1;
             if (t >= kVStages && !__all_sync(kFull, tc::mbar_wait(c.bar(kVe + sv), (t / kVStages - 1) & 1, c.abort_flag))) break;
-            if (!load_tile_zeroed<D>(c, c.base + kOffV + sv * 2 * kRegion, &tmV, kVf + sv, kLand, nland, row, e.y)) break;
+            if (!load_tile_zeroed<D>(c, c.base + kOffV + sv * 2 * kRegion, &m.v, kVf + sv, kLand, nland, row, e.y)) break;
             nv = t + 1;
         }
         int never = 0;
-        for (int m = max(0, nk - kKStages); m < nk; ++m) tc::mbar_wait(c.bar(kKf + m % kKStages), (m / kKStages) & 1, &never);
-        for (int m = max(0, nv - kVStages); m < nv; ++m) tc::mbar_wait(c.bar(kVf + m % kVStages), (m / kVStages) & 1, &never);
+        for (int i = max(0, nk - kKStages); i < nk; ++i) tc::mbar_wait(c.bar(kKf + i % kKStages), (i / kKStages) & 1, &never);
+        for (int i = max(0, nv - kVStages); i < nv; ++i) tc::mbar_wait(c.bar(kVf + i % kVStages), (i / kVStages) & 1, &never);
         tc::mbar_wait(c.bar(kQO), 0, &never);
     } else if (c.warp == 9) {
+        const uint32_t go = tc::elect_one();
         auto wait = [&](int b, int parity) {
             const bool ok = __all_sync(kFull, tc::mbar_wait(c.bar(b), parity & 1, c.abort_flag));
             tc::fence_after_sync();
@@ -679,46 +735,35 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_dq_kernel(const __grid_consta
         };
         auto k = [&](int t) { return c.base + kOffK + (t % kKStages) * 2 * kRegion; };
         auto v = [&](int t) { return c.base + kOffV + (t % kVStages) * 2 * kRegion; };
-        auto tS = [&](int t) { return c.tmem + kTS + 128 * (t & 1); };
-        auto issue_S = [&](int t) {      // S(t) once K(t) has landed; its buffer's reader is done in issue order
+        auto issue_S = [&](int t) {
             if (!wait(kKf + t % kKStages, t / kKStages)) return false;
-            if (c.lane == 0) {
-                mma_rows<D>(tS(t), c.base + kOffQ, k(t));
-                tc::commit(c.bar(kS + (t & 1)));
-            }
-            __syncwarp();
+            mma_rows<D>(c.tmem + kTS, c.base + kOffQ, k(t), go);
+            tc::commit_go(c.bar(kS), go);
             return true;
         };
         auto issue_dP = [&](int t) {
             if (!wait(kVf + t % kVStages, t / kVStages)) return false;
-            if (c.lane == 0) {
-                mma_rows<D>(c.tmem + kTDP, c.base + kOffO, v(t));
-                tc::commit(c.bar(kDP));
-                tc::commit(c.bar(kVe + t % kVStages));
-            }
-            __syncwarp();
+            mma_rows<D>(c.tmem + kTDP, c.base + kOffO, v(t), go);
+            tc::commit_go(c.bar(kDP), go);
+            tc::commit_go(c.bar(kVe + t % kVStages), go);
             return true;
         };
-        bool ok = nt > 0 && wait(kQO, 0) && issue_S(0) && issue_dP(0) && (nt < 2 || issue_S(1));
+        bool ok = nt > 0 && wait(kQO, 0) && issue_S(0) && issue_dP(0);
         for (int t = 0; ok && t < nt; ++t) {
-            if (!wait(kRead, t)) break;                     // dP(t) is in registers
-            if (t + 1 < nt && !issue_dP(t + 1)) break;
+            if (t + 1 < nt && !(wait(kSread, t) && issue_S(t + 1) && wait(kDPread, t) && issue_dP(t + 1))) break;
             if (!wait(kDS, t)) break;
-            if (c.lane == 0) {
-                mma_sums<D>(c.tmem + kTDQ, tS(t), k(t), t > 0);
-                tc::commit(c.bar(kKe + t % kKStages));
-            }
-            __syncwarp();
-            if (t + 2 < nt && !issue_S(t + 2)) break;
+            mma_sums<D>(c.tmem + kTDQ, c.tmem + kTDS, k(t), t > 0, go);
+            tc::commit_go(c.bar(kKe + t % kKStages), go);
+            tc::commit_go(c.bar(kDSfree), go);
         }
-        if (c.lane == 0) tc::commit(c.bar(kDone));
-        __syncwarp();
+        tc::commit_go(c.bar(kDone), go);
         int never = 0;
         tc::mbar_wait(c.bar(kDone), 0, &never);
     } else {
         const int w = c.warp >> 2, r = threadIdx.x & 127;
         const uint32_t lane_off = (uint32_t)((c.warp & 3) * 32) << 16;
-        const uint32_t tDP = c.tmem + kTDP + 64 * w + lane_off;
+        const uint32_t tS = c.tmem + kTS + 64 * w + lane_off, tDP = c.tmem + kTDP + 64 * w + lane_off;
+        const uint32_t tDS = c.tmem + kTDS + 32 * w + lane_off;
         const long long row = (long long)x * p.N + qlo + r;
         const float nl = r < qn ? p.nlse2[row] : -INFINITY, nd = r < qn ? p.nD[row] : 0.f;
         const uint64_t cc = pk2(p.scale_log2, p.scale_log2), nl2 = pk2(nl, nl), nd2 = pk2(nd, nd);
@@ -727,24 +772,22 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_dq_kernel(const __grid_consta
         for (int t = 0; t < nt; ++t) {
             const int valid = valid_next;
             if (t + 1 < nt) valid_next = tile(t + 1).y;
-            const uint32_t tS = c.tmem + kTS + 128 * (t & 1) + 64 * w + lane_off;
-            if (!__all_sync(kFull, tc::mbar_wait(c.bar(kS + (t & 1)), (t >> 1) & 1, c.abort_flag))) { ok = false; break; }
+            if (!__all_sync(kFull, tc::mbar_wait(c.bar(kS), t & 1, c.abort_flag))) { ok = false; break; }
             tc::fence_after_sync();
-            uint32_t pv[2][32];
+            uint32_t pv[2][32], pk[32];
             tc::tmem_ld32(tS, pv[0]);
             tc::tmem_ld32(tS + 32, pv[1]);
             tc::tmem_wait_ld();
             tc::regs_after_wait(pv[0]);
             tc::regs_after_wait(pv[1]);
+            tc::fence_before_sync();
+            tc::mbar_arrive(c.bar(kSread));
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
 #pragma unroll
-                for (int i = 0; i < 32; i += 2) {
-                    float x0, x1;
-                    up2(fma2(pk2(__uint_as_float(pv[h][i]), __uint_as_float(pv[h][i + 1])), cc, nl2), x0, x1);
-                    pv[h][i] = __float_as_uint(ex2(x0));
-                    pv[h][i + 1] = __float_as_uint(ex2(x1));
-                }
+                for (int i = 0; i < 32; i += 2)
+                    ex2_pair(fma2(pk2(__uint_as_float(pv[h][i]), __uint_as_float(pv[h][i + 1])), cc, nl2), i / 2, pv[h][i],
+                             pv[h][i + 1]);
                 if (valid < kTile) {      // keys past the tile's end
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
@@ -753,26 +796,28 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_dq_kernel(const __grid_consta
             }
             if (!__all_sync(kFull, tc::mbar_wait(c.bar(kDP), t & 1, c.abort_flag))) { ok = false; break; }
             tc::fence_after_sync();
+            uint32_t dv[2][32];
+            tc::tmem_ld32(tDP, dv[0]);
+            tc::tmem_ld32(tDP + 32, dv[1]);
+            tc::tmem_wait_ld();
+            tc::regs_after_wait(dv[0]);
+            tc::regs_after_wait(dv[1]);
+            tc::fence_before_sync();
+            tc::mbar_arrive(c.bar(kDPread));
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                uint32_t dv[32], pk[16];
-                tc::tmem_ld32(tDP + 32 * h, dv);
-                tc::tmem_wait_ld();
-                tc::regs_after_wait(dv);
-                if (h == 1) {
-                    tc::fence_before_sync();
-                    tc::mbar_arrive(c.bar(kRead));
-                }
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
                     float x0, x1;
-                    up2(mul2(add2(pk2(__uint_as_float(dv[2 * e]), __uint_as_float(dv[2 * e + 1])), nd2),
+                    up2(mul2(add2(pk2(__uint_as_float(dv[h][2 * e]), __uint_as_float(dv[h][2 * e + 1])), nd2),
                              pk2(__uint_as_float(pv[h][2 * e]), __uint_as_float(pv[h][2 * e + 1]))),
                         x0, x1);
-                    pk[e] = bf16x2(x0, x1);
+                    pk[16 * h + e] = bf16x2(x0, x1);
                 }
-                tc::tmem_st16(tS + 16 * h, pk);
             }
+            if (t > 0 && !__all_sync(kFull, tc::mbar_wait(c.bar(kDSfree), (t - 1) & 1, c.abort_flag))) { ok = false; break; }
+            tc::fence_after_sync();
+            tc::tmem_st32(tDS, pk);
             tc::tmem_wait_st();
             tc::fence_before_sync();
             tc::mbar_arrive(c.bar(kDS));
@@ -785,6 +830,20 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_dq_kernel(const __grid_consta
         }
     }
     cta_finish(c, p.status);
+}
+
+// Both passes in one launch: the CTAs of dK and dV come first, being the longer ones, and those of dQ
+// fill the SMs that they leave idle at their end.
+constexpr int kSmemBytes = kv::kSmem > dq::kSmem ? kv::kSmem : dq::kSmem;
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) bwd_kernel(const __grid_constant__ BwdMaps m, const __grid_constant__ BwdParams p) {
+    extern __shared__ unsigned char smem_raw[];
+    // a CTA that timed out earlier in this launch (or call) makes the rest return at once
+    if (*reinterpret_cast<volatile int*>(p.status) == kDevTimeout) return;
+    const int b = blockIdx.x;
+    if (b < p.kv_blocks) dkv_tile<D>(m, p, smem_raw, b / p.kv_tiles, b % p.kv_tiles);
+    else dq_tile<D>(m, p, smem_raw, (b - p.kv_blocks) / p.q_tiles, (b - p.kv_blocks) % p.q_tiles);
 }
 
 size_t align256(size_t b) { return (b + 255) / 256 * 256; }
@@ -855,23 +914,19 @@ cudaError_t launch_bwd(const AttnBwdArgs& a, cudaStream_t s) {
         p.kcap = l.kcap; p.qcap = l.qcap;
         p.Gq = a.Gq; p.Gk = a.Gk;
     }
-    CUtensorMap mq, mk, mv, mo;
+    BwdMaps m;
     const long long krows = (long long)a.P * a.N;
-    if (!make_tmap_bf16_sw128(&mq, a.Q, rows, D, kTile, 64) || !make_tmap_bf16_sw128(&mk, a.K, krows, D, kTile, 64) ||
-        !make_tmap_bf16_sw128(&mv, a.V, krows, D, kTile, 64) || !make_tmap_bf16_sw128(&mo, a.dO, rows, D, kTile, 64))
+    if (!make_tmap_bf16_sw128(&m.q, a.Q, rows, D, kTile, 64) || !make_tmap_bf16_sw128(&m.k, a.K, krows, D, kTile, 64) ||
+        !make_tmap_bf16_sw128(&m.v, a.V, krows, D, kTile, 64) || !make_tmap_bf16_sw128(&m.o, a.dO, rows, D, kTile, 64))
         return cudaErrorInvalidValue;
-    const unsigned tiles = (unsigned)((a.N + kTile - 1) / kTile);
-    if (a.dQ) {
-        e = cudaFuncSetAttribute(bwd_dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, dq::kSmem);
-        if (e != cudaSuccess) return e;
-        bwd_dq_kernel<D><<<dim3(tiles + (sparse ? a.Gq : 0), a.P * a.g), kThreads, dq::kSmem, s>>>(mq, mk, mv, mo, p);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    }
-    if (a.dK) {
-        e = cudaFuncSetAttribute(bwd_dkv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kv::kSmem);
-        if (e != cudaSuccess) return e;
-        bwd_dkv_kernel<D><<<dim3(tiles + (sparse ? a.Gk : 0), a.P), kThreads, kv::kSmem, s>>>(mq, mk, mv, mo, p);
-    }
+    const int tiles = (a.N + kTile - 1) / kTile;
+    p.kv_tiles = tiles + (sparse ? a.Gk : 0);
+    p.q_tiles = tiles + (sparse ? a.Gq : 0);
+    p.kv_blocks = a.dK ? p.kv_tiles * a.P : 0;
+    const long long blocks = p.kv_blocks + (a.dQ ? (long long)p.q_tiles * a.P * a.g : 0);
+    e = cudaFuncSetAttribute(bwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    if (e != cudaSuccess) return e;
+    bwd_kernel<D><<<(unsigned)blocks, kThreads, kSmemBytes, s>>>(m, p);
     return cudaGetLastError();
 }
 
@@ -881,7 +936,7 @@ size_t attn_bwd_workspace(int P, int g, int N, int d, int Gq, int Gk, bool spars
     return bwd_layout(P, g, N, d, Gq, Gk, sparse).bytes;
 }
 
-int attn_bwd_launches(const AttnBwdArgs& a) { return 1 + (a.rowptr != nullptr) + (a.dQ != nullptr) + (a.dK != nullptr); }
+int attn_bwd_launches(const AttnBwdArgs& a) { return 2 + (a.rowptr != nullptr); }
 
 cudaError_t launch_attn_bwd(const AttnBwdArgs& a, cudaStream_t s) {
     return a.d == 128 ? launch_bwd<128>(a, s) : a.d == 64 ? launch_bwd<64>(a, s) : cudaErrorInvalidValue;
