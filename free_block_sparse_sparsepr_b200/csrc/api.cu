@@ -142,6 +142,9 @@ struct sparsepr_handle_s {
     int launches = 0;
     int device = 0;
     int num_sms = 148;
+    // backward passes: CTAs per tile and workspace bytes, dense [0] and block-sparse [1]
+    spr::BwdParts bwd_parts[2] = {};
+    size_t bwd_bytes[2] = {};
 };
 
 namespace {
@@ -522,6 +525,10 @@ sparsepr_status sparsepr_create(const sparsepr_config* cfg, sparsepr_handle* out
     h->nch = (c.N + kSortChunk - 1) / kSortChunk;
     h->Gmax = c.Gk > c.Gq ? c.Gk : c.Gq;
     h->timing = (c.flags & SPARSEPR_FLAG_STAGE_TIMING) != 0;
+    for (int i = 0; i < 2; ++i) {
+        h->bwd_parts[i] = spr::attn_bwd_parts(h->P, h->g, c.N, c.d, i == 1, h->num_sms);
+        h->bwd_bytes[i] = spr::attn_bwd_workspace(h->P, h->g, c.N, c.d, c.Gq, c.Gk, h->bwd_parts[i], i == 1);
+    }
     const size_t P = h->P, Hp = h->Hp, N = c.N, d = c.d, M = h->M > 0 ? h->M : 1, r = c.r > 0 ? c.r : 1;
     const size_t Gk = c.Gk, Gq = c.Gq;
 #define A_(ptr, n)                                 \
@@ -947,7 +954,7 @@ bool bwd_overlap(sparsepr_handle h, const spr::AttnBwdArgs& a) {
     struct Range { const void* p; size_t n; };
     const Range in[] = {{a.Q, qb}, {a.K, kb}, {a.V, kb}, {a.O, qb}, {a.dO, qb}, {a.lse, (size_t)h->Hp * c.N * sizeof(float)}};
     const Range out[] = {{a.dQ, qb}, {a.dK, kb}, {a.dV, kb},
-                         {a.workspace, spr::attn_bwd_workspace(h->P, h->g, c.N, c.d, c.Gq, c.Gk, a.rowptr != nullptr)}};
+                         {a.workspace, h->bwd_bytes[a.rowptr != nullptr]}};
     auto meet = [](const Range& x, const Range& y) {
         const uintptr_t u = reinterpret_cast<uintptr_t>(x.p), v = reinterpret_cast<uintptr_t>(y.p);
         return x.p && y.p && u < v + y.n && v < u + x.n;
@@ -973,8 +980,7 @@ sparsepr_status attn_bwd_impl(sparsepr_handle h, const void* Q, const void* K, c
     int dev = -1;
     if (cudaGetDevice(&dev) != cudaSuccess || dev != h->device) return SPARSEPR_ERR_INVALID_ARG;
     const sparsepr_config& c = h->cfg;
-    if (workspace_bytes < spr::attn_bwd_workspace(h->P, h->g, c.N, c.d, c.Gq, c.Gk, route != nullptr))
-        return SPARSEPR_ERR_WORKSPACE;
+    if (workspace_bytes < h->bwd_bytes[route != nullptr]) return SPARSEPR_ERR_WORKSPACE;
     spr::AttnBwdArgs a;
     memset(&a, 0, sizeof(a));
     a.Q = static_cast<const bf16*>(Q); a.K = static_cast<const bf16*>(K); a.V = static_cast<const bf16*>(V);
@@ -982,6 +988,7 @@ sparsepr_status attn_bwd_impl(sparsepr_handle h, const void* Q, const void* K, c
     a.dQ = static_cast<bf16*>(dQ); a.dK = static_cast<bf16*>(dK); a.dV = static_cast<bf16*>(dV);
     a.workspace = workspace;
     a.status = h->dev_status;
+    a.parts = h->bwd_parts[route != nullptr];
     a.P = h->P; a.g = h->g; a.N = c.N; a.d = c.d; a.Gq = c.Gq; a.Gk = c.Gk;
     if (route) {
         a.qperm = part->qperm; a.kperm = part->kperm; a.qoff = part->qoff; a.koff = part->koff;
@@ -998,7 +1005,7 @@ sparsepr_status attn_bwd_impl(sparsepr_handle h, const void* Q, const void* K, c
 
 sparsepr_status sparsepr_attn_bwd_workspace(sparsepr_handle h, size_t* bytes) {
     if (!h || !bytes) return SPARSEPR_ERR_INVALID_ARG;
-    *bytes = spr::attn_bwd_workspace(h->P, h->g, h->cfg.N, h->cfg.d, h->cfg.Gq, h->cfg.Gk, true);
+    *bytes = h->bwd_bytes[0] > h->bwd_bytes[1] ? h->bwd_bytes[0] : h->bwd_bytes[1];
     return SPARSEPR_OK;
 }
 

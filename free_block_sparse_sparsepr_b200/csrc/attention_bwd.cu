@@ -30,8 +30,11 @@ struct BwdParams {
     const int32_t *qtile_off, *ktile_off;   // [P][G + 1] 128-row tiles before each group
     int kcap, qcap;                         // list entries per group
     int* status;
+    long long krows, qrows;                 // P N, P g N
     int N, g, Gq, Gk;
     int kv_tiles, q_tiles;                  // most key tiles of a KV head, query tiles of a query head
+    int kv_parts, q_parts;                  // CTAs that share a tile's stream
+    float *kv_part, *q_part;                // their fp32 sums: [part][dV, dK][P N][D], [part][P g N][D]
     int kv_blocks;                          // CTAs of dK and dV, before those of dQ
     float scale, scale_log2;
 };
@@ -43,13 +46,12 @@ struct BwdMaps {
 
 // ---------------------------------------------------------------- per-row terms
 // D_i = dO_i . O_i and -lse_i log2(e), negated as the kernels add them. One 16-byte vector of a
-// row per thread, D / 8 threads a row.
+// row per thread, D / 8 threads a row; `t` counts threads. Reads O and dO once: bound by HBM.
 template <int D>
-__global__ void __launch_bounds__(256) bwd_rows_kernel(const uint4* __restrict__ O, const uint4* __restrict__ dO,
-                                                       const float* __restrict__ lse, float* __restrict__ nlse2,
-                                                       float* __restrict__ nD, long long rows) {
+__device__ __forceinline__ void row_terms(const uint4* __restrict__ O, const uint4* __restrict__ dO,
+                                          const float* __restrict__ lse, float* __restrict__ nlse2,
+                                          float* __restrict__ nD, long long rows, long long t) {
     constexpr int kV = D / 8;
-    const long long t = (long long)blockIdx.x * blockDim.x + threadIdx.x;
     const long long row = t / kV;
     float s = 0.f;
     if (row < rows) {
@@ -76,19 +78,23 @@ __global__ void __launch_bounds__(256) bwd_rows_kernel(const uint4* __restrict__
 // route row; the next P Gk collect the rows that hold their key group (binary search, the kept ids
 // ascend); the last 2 P sum up the tiles of each side's own groups. Ids and offsets out of range
 // are skipped and reported in the status word, so every tile stays inside [0, N).
-__global__ void __launch_bounds__(256) bwd_lists_kernel(const int32_t* __restrict__ rowptr,
-                                                        const int32_t* __restrict__ kg,
-                                                        const int32_t* __restrict__ qoff,
-                                                        const int32_t* __restrict__ koff, int2* klist, int32_t* kcnt,
-                                                        int2* qlist, int32_t* qcnt, int32_t* qtile_off,
-                                                        int32_t* ktile_off, int kcap, int qcap, int P, int N, int Gq,
-                                                        int Gk, int* status) {
-    const int wid = (blockIdx.x * blockDim.x + threadIdx.x) >> 5, lane = threadIdx.x & 31;
+struct ListParams {
+    const int32_t *rowptr, *kg, *qoff, *koff;
+    int2 *klist, *qlist;
+    int32_t *kcnt, *qcnt, *qtile_off, *ktile_off;
+    int* status;
+    int kcap, qcap, P, N, Gq, Gk;
+};
+
+__device__ void tile_lists(const ListParams& l, int wid, int lane) {
+    const int32_t *rowptr = l.rowptr, *kg = l.kg, *qoff = l.qoff, *koff = l.koff;
+    const int P = l.P, N = l.N, Gq = l.Gq, Gk = l.Gk;
+    int* status = l.status;
     if (wid >= P * (Gq + Gk)) {
         const int i = wid - P * (Gq + Gk), z = i >> 1, G = (i & 1) ? Gk : Gq;
         if (z >= P) return;
         const int32_t* off = (i & 1) ? koff + (long long)z * (Gk + 1) : qoff + (long long)z * (Gq + 1);
-        int32_t* out = (i & 1) ? ktile_off + (long long)z * (Gk + 1) : qtile_off + (long long)z * (Gq + 1);
+        int32_t* out = (i & 1) ? l.ktile_off + (long long)z * (Gk + 1) : l.qtile_off + (long long)z * (Gq + 1);
         bool bad = false;
         int before = 0;
         for (int g0 = 0; g0 < G; g0 += 32) {
@@ -116,8 +122,8 @@ __global__ void __launch_bounds__(256) bwd_lists_kernel(const int32_t* __restric
     const int32_t* rp = rowptr + (long long)z * (Gq + 1);
     const int32_t* kept = kg + (long long)z * Gq * Gk;
     const int32_t* off = rows ? koff + (long long)z * (Gk + 1) : qoff + (long long)z * (Gq + 1);
-    const int cap = rows ? kcap : qcap;
-    int2* out = (rows ? klist + ((long long)z * Gq + own) * cap : qlist + ((long long)z * Gk + own) * cap);
+    const int cap = rows ? l.kcap : l.qcap;
+    int2* out = (rows ? l.klist + ((long long)z * Gq + own) * cap : l.qlist + ((long long)z * Gk + own) * cap);
     bool bad = false;
     // the bounds of route row a, empty if they are no range of the kept list
     auto row_range = [&](int a) {
@@ -182,8 +188,19 @@ __global__ void __launch_bounds__(256) bwd_lists_kernel(const int32_t* __restric
         }
     }
     emit();
-    if (lane == 0) (rows ? kcnt + (long long)z * Gq : qcnt + (long long)z * Gk)[own] = nt;
+    if (lane == 0) (rows ? l.kcnt + (long long)z * Gq : l.qcnt + (long long)z * Gk)[own] = nt;
     if (__any_sync(kFull, bad) && lane == 0) set_status(status, kDevBounds);
+}
+
+// The lists (blocks before `list_blocks`) and the rows' terms (the others) in one launch.
+template <int D>
+__global__ void __launch_bounds__(256) bwd_prepare_kernel(const ListParams l, int list_blocks, const uint4* O, const uint4* dO,
+                                                          const float* lse, float* nlse2, float* nD, long long rows) {
+    if ((int)blockIdx.x < list_blocks) {
+        tile_lists(l, (blockIdx.x * blockDim.x + threadIdx.x) >> 5, threadIdx.x & 31);
+        return;
+    }
+    row_terms<D>(O, dO, lse, nlse2, nD, rows, (long long)(blockIdx.x - list_blocks) * blockDim.x + threadIdx.x);
 }
 
 // ---------------------------------------------------------------- gradients
@@ -413,6 +430,27 @@ __device__ __forceinline__ void store_acc_row(uint32_t tacc, float scale, bf16* 
     }
 }
 
+// The same row as it is, into fp32 partial sums.
+template <int D>
+__device__ __forceinline__ void store_part_row(uint32_t tacc, float* out, bool zero) {
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) {
+        uint32_t v[32];
+        tc::tmem_ld32(tacc + 32 * c, v);
+        tc::tmem_wait_ld();
+        tc::regs_after_wait(v);
+        if (!out) continue;
+#pragma unroll
+        for (int i = 0; i < 32; i += 8) {
+            if (zero)
+                for (int e = 0; e < 8; ++e) v[i + e] = 0u;
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(out + 32 * c + i), "r"(v[i]),
+                         "r"(v[i + 1]), "r"(v[i + 2]), "r"(v[i + 3]), "r"(v[i + 4]), "r"(v[i + 5]), "r"(v[i + 6]), "r"(v[i + 7])
+                         : "memory");
+        }
+    }
+}
+
 // Output row of position `pos` (null: out of range, reported, or not wanted).
 template <int D>
 __device__ __forceinline__ bf16* out_row(bf16* base, const int32_t* perm, long long head, int N, int pos, bool want,
@@ -472,14 +510,17 @@ static_assert(kSmem <= 232448, "shared memory budget");
 constexpr uint32_t kTS = 0, kTP = 128, kTDS = 192, kTDV = 256, kTDK = 384;      // dP: the columns of S
 }  // namespace kv
 
-template <int D>
-__device__ __forceinline__ void dkv_tile(const BwdMaps& m, const BwdParams& p, unsigned char* smem_raw, int z, int pair) {
+template <int D, bool PARTS>
+__device__ __forceinline__ void dkv_tile(const BwdMaps& m, const BwdParams& p, unsigned char* smem_raw, int z, int pair, int part) {
     using namespace kv;
     int grp, klo, kn;
     if (!find_tile(p.koff, p.ktile_off, z, p.Gk, p.N, pair, grp, klo, kn)) return;
     const int2* list = p.qlist + ((long long)z * p.Gk + grp) * p.qcap;
     const int nt = p.qcnt ? p.qcnt[(long long)z * p.Gk + grp] : (p.N + kTile - 1) / kTile;
-    const int iters = nt * p.g;
+    // this CTA's share of the (query head, query tile) stream
+    const long long all = (long long)nt * p.g;
+    const int first = PARTS ? (int)(all * part / p.kv_parts) : 0;
+    const int iters = PARTS ? (int)(all * (part + 1) / p.kv_parts) - first : (int)all;
     auto tile = [&](int t) { return p.qcnt ? list[t] : make_int2(t * kTile, min(kTile, p.N - t * kTile)); };
     {
         // ones under the parts of -lse (columns 0-2), or under those of -D (3-5); the halves of columns
@@ -507,7 +548,7 @@ __device__ __forceinline__ void dkv_tile(const BwdMaps& m, const BwdParams& p, u
             }
         }
         __syncwarp();
-        int nland = 0, nq = 0, no = 0, t = 0, x = z * p.g;
+        int nland = 0, nq = 0, no = 0, t = PARTS && nt ? first % nt : 0, x = z * p.g + (PARTS && nt ? first / nt : 0);
         // this lane's four rows of the next tile's terms; rows past its end give P = 2^(-huge) = 0
         float nl[4], nd[4];
         auto fetch = [&](int2 e, int head) {
@@ -520,7 +561,7 @@ __device__ __forceinline__ void dkv_tile(const BwdMaps& m, const BwdParams& p, u
             }
         };
         const float inv = 1.f / p.scale_log2;
-        int2 e = iters > 0 ? tile(0) : make_int2(0, 0);
+        int2 e = iters > 0 ? tile(t) : make_int2(0, 0);
         if (iters > 0) fetch(e, x);
         for (int it = 0; it < iters; ++it) {
             const int s = it % kStages, row = x * p.N + e.x, valid = e.y;
@@ -669,8 +710,14 @@ __device__ __forceinline__ void dkv_tile(const BwdMaps& m, const BwdParams& p, u
         // warpgroup 0 stores dV, warpgroup 1 dK
         if (__all_sync(kFull, ok && tc::mbar_wait(c.bar(kDone), 0, c.abort_flag))) {
             tc::fence_after_sync();
-            bf16* out = out_row<D>(w ? p.dK : p.dV, p.kperm, z, p.N, klo + r, r < kn, z, p.status);
-            store_acc_row<D>(c.tmem + (w ? kTDK : kTDV) + lane_off, w ? p.scale : 1.f, out, iters == 0);
+            const uint32_t acc = c.tmem + (w ? kTDK : kTDV) + lane_off;
+            if (PARTS && p.kv_parts > 1) {
+                const long long row = (part * 2 + w) * p.krows + (long long)z * p.N + klo + r;
+                store_part_row<D>(acc, r < kn ? p.kv_part + row * D : nullptr, iters == 0);
+            } else {
+                bf16* out = out_row<D>(w ? p.dK : p.dV, p.kperm, z, p.N, klo + r, r < kn, z, p.status);
+                store_acc_row<D>(acc, w ? p.scale : 1.f, out, iters == 0);
+            }
         }
     }
     cta_finish(c, p.status);
@@ -691,15 +738,21 @@ static_assert(kSmem <= 232448, "shared memory budget");
 constexpr uint32_t kTS = 0, kTDP = 128, kTDQ = 256, kTDS = 384;
 }  // namespace dq
 
-template <int D>
-__device__ __forceinline__ void dq_tile(const BwdMaps& m, const BwdParams& p, unsigned char* smem_raw, int x, int pair) {
+template <int D, bool PARTS>
+__device__ __forceinline__ void dq_tile(const BwdMaps& m, const BwdParams& p, unsigned char* smem_raw, int x, int pair, int part) {
     using namespace dq;
     const int z = x / p.g;
     int grp, qlo, qn;
     if (!find_tile(p.qoff, p.qtile_off, z, p.Gq, p.N, pair, grp, qlo, qn)) return;
     const int2* list = p.klist + ((long long)z * p.Gq + grp) * p.kcap;
-    const int nt = p.kcnt ? p.kcnt[(long long)z * p.Gq + grp] : (p.N + kTile - 1) / kTile;
-    auto tile = [&](int t) { return p.kcnt ? list[t] : make_int2(t * kTile, min(kTile, p.N - t * kTile)); };
+    // this CTA's share of the key tiles
+    const int all = p.kcnt ? p.kcnt[(long long)z * p.Gq + grp] : (p.N + kTile - 1) / kTile;
+    const int first = PARTS ? (int)((long long)all * part / p.q_parts) : 0;
+    const int nt = PARTS ? (int)((long long)all * (part + 1) / p.q_parts) - first : all;
+    auto tile = [&](int t) {
+        t += first;
+        return p.kcnt ? list[t] : make_int2(t * kTile, min(kTile, p.N - t * kTile));
+    };
     const Cta c = cta_setup(smem_raw, kOffBar, kBars, [](int i) { return i >= kSread ? 256 : 1; });
 
     if (c.warp == 8) {
@@ -825,8 +878,14 @@ __device__ __forceinline__ void dq_tile(const BwdMaps& m, const BwdParams& p, un
         if (__all_sync(kFull, ok && tc::mbar_wait(c.bar(kDone), 0, c.abort_flag))) {
             tc::fence_after_sync();
             // each warpgroup stores half of the row's columns
-            bf16* out = out_row<D>(p.dQ, p.qperm, x, p.N, qlo + r, r < qn, z, p.status);
-            store_acc_row<D / 2>(c.tmem + kTDQ + w * (D / 2) + lane_off, p.scale, out ? out + w * (D / 2) : nullptr, nt == 0);
+            const uint32_t acc = c.tmem + kTDQ + w * (D / 2) + lane_off;
+            if (PARTS && p.q_parts > 1) {
+                float* out = p.q_part + (part * p.qrows + (long long)x * p.N + qlo + r) * D + w * (D / 2);
+                store_part_row<D / 2>(acc, r < qn ? out : nullptr, nt == 0);
+            } else {
+                bf16* out = out_row<D>(p.dQ, p.qperm, x, p.N, qlo + r, r < qn, z, p.status);
+                store_acc_row<D / 2>(acc, p.scale, out ? out + w * (D / 2) : nullptr, nt == 0);
+            }
         }
     }
     cta_finish(c, p.status);
@@ -836,25 +895,62 @@ __device__ __forceinline__ void dq_tile(const BwdMaps& m, const BwdParams& p, un
 // fill the SMs that they leave idle at their end.
 constexpr int kSmemBytes = kv::kSmem > dq::kSmem ? kv::kSmem : dq::kSmem;
 
-template <int D>
+template <int D, bool PARTS>
 __global__ void __launch_bounds__(kThreads, 1) bwd_kernel(const __grid_constant__ BwdMaps m, const __grid_constant__ BwdParams p) {
     extern __shared__ unsigned char smem_raw[];
     // a CTA that timed out earlier in this launch (or call) makes the rest return at once
     if (*reinterpret_cast<volatile int*>(p.status) == kDevTimeout) return;
     const int b = blockIdx.x;
-    if (b < p.kv_blocks) dkv_tile<D>(m, p, smem_raw, b / p.kv_tiles, b % p.kv_tiles);
-    else dq_tile<D>(m, p, smem_raw, (b - p.kv_blocks) / p.q_tiles, (b - p.kv_blocks) % p.q_tiles);
+    if (b < p.kv_blocks) {
+        const int t = PARTS ? b / p.kv_parts : b;
+        dkv_tile<D, PARTS>(m, p, smem_raw, t / p.kv_tiles, t % p.kv_tiles, PARTS ? b % p.kv_parts : 0);
+    } else {
+        const int i = b - p.kv_blocks, t = PARTS ? i / p.q_parts : i;
+        dq_tile<D, PARTS>(m, p, smem_raw, t / p.q_tiles, t % p.q_tiles, PARTS ? i % p.q_parts : 0);
+    }
+}
+
+// Sums of the parts in their order, scaled, rounded and written to the output rows: D / 8 threads a row.
+template <int D>
+__global__ void __launch_bounds__(256) bwd_join_kernel(const __grid_constant__ BwdParams p) {
+    const long long t = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+    long long row = t / (D / 8);
+    const int col = (int)(t % (D / 8)) * 8;
+    const long long kv = p.kv_parts > 1 && p.dK ? 2 * p.krows : 0;
+    const bool q = row >= kv;
+    if (q) row -= kv;
+    if (q && (p.q_parts <= 1 || !p.dQ || row >= p.qrows)) return;
+    const int parts = q ? p.q_parts : p.kv_parts;
+    const long long step = (q ? p.qrows : 2 * p.krows) * D;
+    const float* src = (q ? p.q_part : p.kv_part) + row * D + col;
+    float s[8] = {};
+    for (int i = 0; i < parts; ++i, src += step) {
+        const float4 a = __ldg(reinterpret_cast<const float4*>(src)), b = __ldg(reinterpret_cast<const float4*>(src) + 1);
+        const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s[e] += v[e];
+    }
+    const bool is_dv = !q && row < p.krows;
+    if (!q && !is_dv) row -= p.krows;
+    const float scale = is_dv ? 1.f : p.scale;
+    const long long head = row / p.N, z = q ? head / p.g : head;
+    bf16* out = out_row<D>(q ? p.dQ : is_dv ? p.dV : p.dK, q ? p.qperm : p.kperm, head, p.N, (int)(row % p.N), true, z, p.status);
+    if (!out) return;
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[e] = bf16x2(s[2 * e] * scale, s[2 * e + 1] * scale);
+    *reinterpret_cast<uint4*>(out + col) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 size_t align256(size_t b) { return (b + 255) / 256 * 256; }
 
 // Byte offsets of the workspace's parts.
 struct BwdLayout {
-    size_t nlse2, nD, klist, qlist, kcnt, qcnt, qtile_off, ktile_off, bytes;
+    size_t nlse2, nD, kv_part, q_part, klist, qlist, kcnt, qcnt, qtile_off, ktile_off, bytes;
     int kcap, qcap;
 };
 
-BwdLayout bwd_layout(int P, int g, int N, int d, int Gq, int Gk, bool sparse) {
+BwdLayout bwd_layout(int P, int g, int N, int d, int Gq, int Gk, const BwdParts& parts, bool sparse) {
     BwdLayout l;
     memset(&l, 0, sizeof(l));
     size_t at = 0;
@@ -866,6 +962,8 @@ BwdLayout bwd_layout(int P, int g, int N, int d, int Gq, int Gk, bool sparse) {
     const size_t rows = (size_t)P * g * N * sizeof(float), tiles = (size_t)((N + kTile - 1) / kTile);
     l.nlse2 = take(rows);
     l.nD = take(rows);
+    if (parts.kv > 1) l.kv_part = take((size_t)parts.kv * 2 * P * N * d * sizeof(float));
+    if (parts.q > 1) l.q_part = take((size_t)parts.q * P * g * N * d * sizeof(float));
     if (sparse) {
         // the runs of a list are disjoint: at most N / 128 full tiles and one ragged tile per group
         l.kcap = (int)(tiles + Gk);
@@ -884,59 +982,113 @@ BwdLayout bwd_layout(int P, int g, int N, int d, int Gq, int Gk, bool sparse) {
 template <int D>
 cudaError_t launch_bwd(const AttnBwdArgs& a, cudaStream_t s) {
     const bool sparse = a.rowptr != nullptr;
-    const BwdLayout l = bwd_layout(a.P, a.g, a.N, D, a.Gq, a.Gk, sparse);
+    const BwdLayout l = bwd_layout(a.P, a.g, a.N, D, a.Gq, a.Gk, a.parts, sparse);
     char* ws = static_cast<char*>(a.workspace);
     float *nlse2 = reinterpret_cast<float*>(ws + l.nlse2), *nD = reinterpret_cast<float*>(ws + l.nD);
-    const long long rows = (long long)a.P * a.g * a.N;
-    bwd_rows_kernel<D><<<(unsigned)((rows * (D / 8) + 255) / 256), 256, 0, s>>>(
-        reinterpret_cast<const uint4*>(a.O), reinterpret_cast<const uint4*>(a.dO), a.lse, nlse2, nD, rows);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
+    const long long rows = (long long)a.P * a.g * a.N, krows = (long long)a.P * a.N;
     BwdParams p;
     memset(&p, 0, sizeof(p));
     p.nlse2 = nlse2; p.nD = nD;
     p.dQ = a.dQ; p.dK = a.dK; p.dV = a.dV;
+    p.krows = krows; p.qrows = rows;
     p.N = a.N; p.g = a.g; p.Gq = 1; p.Gk = 1;
+    p.kv_parts = a.parts.kv; p.q_parts = a.parts.q;
+    p.kv_part = reinterpret_cast<float*>(ws + l.kv_part); p.q_part = reinterpret_cast<float*>(ws + l.q_part);
     p.status = a.status;
     p.scale = (float)(1.0 / sqrt((double)D));
     p.scale_log2 = (float)(1.4426950408889634 / sqrt((double)D));
+    ListParams lp;
+    memset(&lp, 0, sizeof(lp));
+    int list_blocks = 0;
     if (sparse) {
-        int2 *klist = reinterpret_cast<int2*>(ws + l.klist), *qlist = reinterpret_cast<int2*>(ws + l.qlist);
-        int32_t *kcnt = reinterpret_cast<int32_t*>(ws + l.kcnt), *qcnt = reinterpret_cast<int32_t*>(ws + l.qcnt);
-        int32_t *qt = reinterpret_cast<int32_t*>(ws + l.qtile_off), *kt = reinterpret_cast<int32_t*>(ws + l.ktile_off);
-        const long long warps = (long long)a.P * (a.Gq + a.Gk + 2);
-        bwd_lists_kernel<<<(unsigned)((warps * 32 + 255) / 256), 256, 0, s>>>(
-            a.rowptr, a.kg, a.qoff, a.koff, klist, kcnt, qlist, qcnt, qt, kt, l.kcap, l.qcap, a.P, a.N, a.Gq, a.Gk, a.status);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        lp.rowptr = a.rowptr; lp.kg = a.kg; lp.qoff = a.qoff; lp.koff = a.koff;
+        lp.klist = reinterpret_cast<int2*>(ws + l.klist); lp.qlist = reinterpret_cast<int2*>(ws + l.qlist);
+        lp.kcnt = reinterpret_cast<int32_t*>(ws + l.kcnt); lp.qcnt = reinterpret_cast<int32_t*>(ws + l.qcnt);
+        lp.qtile_off = reinterpret_cast<int32_t*>(ws + l.qtile_off);
+        lp.ktile_off = reinterpret_cast<int32_t*>(ws + l.ktile_off);
+        lp.status = a.status;
+        lp.kcap = l.kcap; lp.qcap = l.qcap; lp.P = a.P; lp.N = a.N; lp.Gq = a.Gq; lp.Gk = a.Gk;
+        list_blocks = (int)(((long long)a.P * (a.Gq + a.Gk + 2) * 32 + 255) / 256);
         p.qoff = a.qoff; p.koff = a.koff; p.qperm = a.qperm; p.kperm = a.kperm;
-        p.klist = klist; p.qlist = qlist; p.kcnt = kcnt; p.qcnt = qcnt;
-        p.qtile_off = qt; p.ktile_off = kt;
+        p.klist = lp.klist; p.qlist = lp.qlist; p.kcnt = lp.kcnt; p.qcnt = lp.qcnt;
+        p.qtile_off = lp.qtile_off; p.ktile_off = lp.ktile_off;
         p.kcap = l.kcap; p.qcap = l.qcap;
         p.Gq = a.Gq; p.Gk = a.Gk;
     }
+    const long long row_blocks = (rows * (D / 8) + 255) / 256;
+    bwd_prepare_kernel<D><<<(unsigned)(list_blocks + row_blocks), 256, 0, s>>>(
+        lp, list_blocks, reinterpret_cast<const uint4*>(a.O), reinterpret_cast<const uint4*>(a.dO), a.lse, nlse2, nD, rows);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
     BwdMaps m;
-    const long long krows = (long long)a.P * a.N;
     if (!make_tmap_bf16_sw128(&m.q, a.Q, rows, D, kTile, 64) || !make_tmap_bf16_sw128(&m.k, a.K, krows, D, kTile, 64) ||
         !make_tmap_bf16_sw128(&m.v, a.V, krows, D, kTile, 64) || !make_tmap_bf16_sw128(&m.o, a.dO, rows, D, kTile, 64))
         return cudaErrorInvalidValue;
     const int tiles = (a.N + kTile - 1) / kTile;
     p.kv_tiles = tiles + (sparse ? a.Gk : 0);
     p.q_tiles = tiles + (sparse ? a.Gq : 0);
-    p.kv_blocks = a.dK ? p.kv_tiles * a.P : 0;
-    const long long blocks = p.kv_blocks + (a.dQ ? (long long)p.q_tiles * a.P * a.g : 0);
-    e = cudaFuncSetAttribute(bwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    p.kv_blocks = a.dK ? p.kv_tiles * a.P * p.kv_parts : 0;
+    const long long blocks = p.kv_blocks + (a.dQ ? (long long)p.q_tiles * a.P * a.g * p.q_parts : 0);
+    const auto kernel = p.kv_parts > 1 || p.q_parts > 1 ? bwd_kernel<D, true> : bwd_kernel<D, false>;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
     if (e != cudaSuccess) return e;
-    bwd_kernel<D><<<(unsigned)blocks, kThreads, kSmemBytes, s>>>(m, p);
+    kernel<<<(unsigned)blocks, kThreads, kSmemBytes, s>>>(m, p);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    const long long join = (p.kv_parts > 1 && a.dK ? 2 * krows : 0) + (p.q_parts > 1 && a.dQ ? rows : 0);
+    if (join) bwd_join_kernel<D><<<(unsigned)((join * (D / 8) + 255) / 256), 256, 0, s>>>(p);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-size_t attn_bwd_workspace(int P, int g, int N, int d, int Gq, int Gk, bool sparse) {
-    return bwd_layout(P, g, N, d, Gq, Gk, sparse).bytes;
+// How many CTAs share a tile's stream: the pair that a model of the launch expects to end first. An
+// SM runs one CTA at a time, those of dK/dV first. Times in microseconds at 1.9 GHz: 1.42 for a dK/dV
+// tile, 1.0 for a dQ tile, 2.5 for a CTA's start and end; the join of the parts' sums takes 2.5 for its
+// launch and 1 per 4 MB written and read back. Few CTAs with long streams gain most, and a number of
+// CTAs just past a multiple of the SMs is stepped over. On the device, whole against shared (d = 128, one
+// sample): 4 query heads on 1 KV head, 1000 tokens 54 against 17 us; 3 on 1, 4096 tokens 142 against 85;
+// 12 heads, 1024 tokens 30 against 45 (left whole).
+BwdParts attn_bwd_parts(int P, int g, int N, int d, bool sparse, int sms) {
+    BwdParts best = {1, 1};
+    const double tiles = (N + kTile - 1) / kTile;
+    // of a route neither the density nor the groups' sizes are known here: a quarter of the keys, and
+    // a quarter more tiles than whole ones
+    const double len = sparse ? ceil(tiles / 4) : tiles, ctas = sparse ? ceil(1.25 * tiles) : tiles;
+    if (ctas * P > 8.0 * sms) return best;
+    static const int kChoices[] = {1, 2, 3, 4, 6, 8, 12, 16};
+    double best_t = 1e30;
+    for (int kv : kChoices)
+        for (int q : kChoices) {
+            if ((kv > 1 && kv > len * g) || (q > 1 && q > len)) continue;
+            const double nk = ctas * P * kv, nq = ctas * P * g * q, tk = 1.42 * ceil(len * g / kv) + 2.5, tq = ceil(len / q) + 2.5;
+            const double whole = floor(nk / sms), rest = nk - whole * sms;     // `rest` SMs run one dK/dV CTA more
+            // the dQ CTAs start at whole tk on the other SMs and at (whole + 1) tk on those
+            double t = (nk * tk + nq * tq) / sms;
+            t = fmax(t, (rest > 0 ? whole + 1 : whole) * tk);
+            auto fit = [&](double end) {
+                const double late = floor((end - (whole + 1) * tk) / tq + 1e-6), early = floor((end - whole * tk) / tq + 1e-6);
+                return rest * fmax(late, 0.0) + (sms - rest) * fmax(early, 0.0);
+            };
+            for (int i = 0; i < 32 && fit(t) < nq; ++i) {      // on to the next end of a dQ CTA
+                const double e0 = (floor((t - whole * tk) / tq + 1e-6) + 1) * tq + whole * tk;
+                const double e1 = rest > 0 ? (floor((t - (whole + 1) * tk) / tq + 1e-6) + 1) * tq + (whole + 1) * tk : e0;
+                t = fmin(e0, e1);
+            }
+            const double mb = 4e-6 * d * N * (double)P * ((kv > 1 ? 2.0 * kv : 0) + (q > 1 ? (double)g * q : 0));
+            if (kv > 1 || q > 1) t += 2.5 + 2 * mb / 4;
+            if (t < best_t * 0.97) {      // a gain below the model's error is none
+                best_t = t;
+                best = {kv, q};
+            }
+        }
+    return best;
 }
 
-int attn_bwd_launches(const AttnBwdArgs& a) { return 2 + (a.rowptr != nullptr); }
+size_t attn_bwd_workspace(int P, int g, int N, int d, int Gq, int Gk, const BwdParts& parts, bool sparse) {
+    return bwd_layout(P, g, N, d, Gq, Gk, parts, sparse).bytes;
+}
+
+int attn_bwd_launches(const AttnBwdArgs& a) { return 2 + ((a.dK && a.parts.kv > 1) || (a.dQ && a.parts.q > 1)); }
 
 cudaError_t launch_attn_bwd(const AttnBwdArgs& a, cudaStream_t s) {
     return a.d == 128 ? launch_bwd<128>(a, s) : a.d == 64 ? launch_bwd<64>(a, s) : cudaErrorInvalidValue;

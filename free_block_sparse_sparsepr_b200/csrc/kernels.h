@@ -188,6 +188,10 @@ cudaError_t launch_attn_probe(const bf16* Q, const bf16* K, const bf16* V, const
 // heads each. Q, K, V, O, lse and dO as the forward pass takes and leaves them (group-major for the
 // block-sparse pass); dQ, dK, dV in original order (row qperm / kperm of each position). dQ null
 // skips it, dK and dV null skips both. workspace: attn_bwd_workspace bytes, 256-byte aligned parts.
+struct BwdParts {
+    int kv, q;                           // CTAs that share the stream of a dK/dV tile, of a dQ tile
+};
+BwdParts attn_bwd_parts(int P, int g, int N, int d, bool sparse, int sms);
 struct AttnBwdArgs {
     const bf16 *Q, *K, *V, *O, *dO;
     const float* lse;
@@ -195,9 +199,10 @@ struct AttnBwdArgs {
     bf16 *dQ, *dK, *dV;
     void* workspace;
     int* status;
+    BwdParts parts;
     int P, g, N, d, Gq, Gk;
 };
-size_t attn_bwd_workspace(int P, int g, int N, int d, int Gq, int Gk, bool sparse);
+size_t attn_bwd_workspace(int P, int g, int N, int d, int Gq, int Gk, const BwdParts& parts, bool sparse);
 int attn_bwd_launches(const AttnBwdArgs& a);
 cudaError_t launch_attn_bwd(const AttnBwdArgs& a, cudaStream_t s);
 

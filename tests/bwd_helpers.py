@@ -62,7 +62,8 @@ def backward_reference(Q, K, V, O, lse, dO, masks=None):
     """The fp64 gradients, and per gradient a worst-case bound and an rms estimate of the kernels' error.
 
     The kernels form logits, dO.v and D in fp32 (d products each, at most one step 2^-23 a product),
-    P = 2^x with a relative error of the exponent's absolute error plus 2^-21, round P and dS to
+    P = 2^x with a relative error of the exponent's absolute error plus 2^-18 (a polynomial that is
+    2^-18.5 off at most, after roundings of its five terms below 2^-21 together), round P and dS to
     bf16 (2^-8 of their value) as operands, sum in fp32 over n pairs (n steps of the sum of
     magnitudes) and round the result to bf16. The worst case adds all magnitudes; the rms estimate
     adds the squares of the operand roundings, taken at their full half step, so that it holds for
@@ -91,7 +92,7 @@ def backward_reference(Q, K, V, O, lse, dO, masks=None):
             dS = P * (dP - D)
             # relative error of P; absolute error of dS before its rounding
             finite_ls = torch.where(ls.isfinite(), ls, 0.0)
-            eP = scale * d * E_F32 * (q.abs() @ k.abs().T) + 4 * E_F32 * (s.abs() + finite_ls.abs()) + 2.0 ** -21
+            eP = scale * d * E_F32 * (q.abs() @ k.abs().T) + 4 * E_F32 * (s.abs() + finite_ls.abs()) + 2.0 ** -18
             eS = P * (eP * (dP - D).abs() + d * E_F32 * (do.abs() @ v.abs().T + (do.abs() * o.abs()).sum(1, keepdim=True)))
             rP, rS = U_BF16 * P, U_BF16 * dS.abs()
             out["dV"][b, z] += P.T @ do
