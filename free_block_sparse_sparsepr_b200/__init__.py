@@ -177,10 +177,18 @@ def _on(device, stream):
 def _stream_on(device, stream) -> int:
     """_stream on a given device (looking that device up anew costs microseconds a call)."""
     if stream is None:
-        import torch
-
-        return torch.cuda.current_stream(device.index).cuda_stream
+        return _current_raw_stream(device.index)
     return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _current_raw_stream(index: int) -> int:
+    """The current stream's pointer; torch's Stream object costs a microsecond where its raw getter is not there."""
+    global _current_raw_stream
+    import torch
+
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    _current_raw_stream = raw or (lambda i: torch.cuda.current_stream(i).cuda_stream)
+    return _current_raw_stream(index)
 
 
 def _want(name, t, shape, dtype, device):
@@ -393,10 +401,10 @@ class SparsePR:
             raise ValueError(f"workspace: expected contiguous memory on {dev}")
         with _on(dev, stream):
             if need_dq and dQ is None:
-                dQ = torch.empty(qs, dtype=bf16, device=dev)
+                dQ = torch.empty_like(Q)
             if need_dkv:
-                dK = torch.empty(ks, dtype=bf16, device=dev) if dK is None else dK
-                dV = torch.empty(ks, dtype=bf16, device=dev) if dV is None else dV
+                dK = torch.empty_like(K) if dK is None else dK
+                dV = torch.empty_like(V) if dV is None else dV
             if workspace is None:
                 workspace = torch.empty(self._bwd_bytes, dtype=torch.uint8, device=dev)
             _check(name, call(Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(), lse.data_ptr(), dO.data_ptr(),

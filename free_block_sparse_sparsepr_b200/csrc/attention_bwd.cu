@@ -9,6 +9,8 @@
 #include <math.h>
 #include <string.h>
 
+#include <atomic>
+
 #include "common.cuh"
 #include "kernels.h"
 #include "tc_primitives.cuh"
@@ -1029,9 +1031,17 @@ cudaError_t launch_bwd(const AttnBwdArgs& a, cudaStream_t s) {
     p.q_tiles = tiles + (sparse ? a.Gq : 0);
     p.kv_blocks = a.dK ? p.kv_tiles * a.P * p.kv_parts : 0;
     const long long blocks = p.kv_blocks + (a.dQ ? (long long)p.q_tiles * a.P * a.g * p.q_parts : 0);
-    const auto kernel = p.kv_parts > 1 || p.q_parts > 1 ? bwd_kernel<D, true> : bwd_kernel<D, false>;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-    if (e != cudaSuccess) return e;
+    const bool parts = p.kv_parts > 1 || p.q_parts > 1;
+    const auto kernel = parts ? bwd_kernel<D, true> : bwd_kernel<D, false>;
+    // the attribute stays with the kernel on its device: set once (setting it twice at once does no harm)
+    static std::atomic<unsigned long long> have[2];
+    int dev = 0;
+    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+    if (dev >= 64 || !(have[parts].load() >> dev & 1)) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) have[parts] |= 1ull << dev;
+    }
     kernel<<<(unsigned)blocks, kThreads, kSmemBytes, s>>>(m, p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     const long long join = (p.kv_parts > 1 && a.dK ? 2 * krows : 0) + (p.q_parts > 1 && a.dQ ? rows : 0);
