@@ -26,10 +26,9 @@ struct BwdParams {
     const float *nlse2, *nD;                // per query row: -lse log2(e), -dO.O
     bf16 *dQ, *dK, *dV;
     const int32_t *qperm, *kperm;           // output row of each position (null: the position itself)
-    const int32_t *qoff, *koff;             // group offsets (null: one group of N rows)
     const int2 *klist, *qlist;              // kept key tiles of each query group, query tiles of each key group
     const int32_t *kcnt, *qcnt;             // their numbers
-    const int32_t *qtile_off, *ktile_off;   // [P][G + 1] 128-row tiles before each group
+    const int4 *qtile, *ktile;              // [P][q_tiles], [P][kv_tiles]: group, first row and rows of each tile (0: none)
     int kcap, qcap;                         // list entries per group
     int* status;
     long long krows, qrows;                 // P N, P g N
@@ -78,14 +77,15 @@ __device__ __forceinline__ void row_terms(const uint4* __restrict__ O, const uin
 // One warp per (KV head z, group): the tiles (start row, valid rows <= 128) of the other side's
 // groups that the route pairs with it, runs of touching groups merged. Warps [0, P Gq) walk their
 // route row; the next P Gk collect the rows that hold their key group (binary search, the kept ids
-// ascend); the last 2 P sum up the tiles of each side's own groups. Ids and offsets out of range
+// ascend); the last 2 P cut each side's own groups into tiles. Ids and offsets out of range
 // are skipped and reported in the status word, so every tile stays inside [0, N).
 struct ListParams {
     const int32_t *rowptr, *kg, *qoff, *koff;
     int2 *klist, *qlist;
-    int32_t *kcnt, *qcnt, *qtile_off, *ktile_off;
+    int32_t *kcnt, *qcnt;
+    int4 *qtile, *ktile;
     int* status;
-    int kcap, qcap, P, N, Gq, Gk;
+    int kcap, qcap, q_tiles, kv_tiles, P, N, Gq, Gk;
 };
 
 __device__ void tile_lists(const ListParams& l, int wid, int lane) {
@@ -96,13 +96,15 @@ __device__ void tile_lists(const ListParams& l, int wid, int lane) {
         const int i = wid - P * (Gq + Gk), z = i >> 1, G = (i & 1) ? Gk : Gq;
         if (z >= P) return;
         const int32_t* off = (i & 1) ? koff + (long long)z * (Gk + 1) : qoff + (long long)z * (Gq + 1);
-        int32_t* out = (i & 1) ? l.ktile_off + (long long)z * (Gk + 1) : l.qtile_off + (long long)z * (Gq + 1);
+        const int cap = (i & 1) ? l.kv_tiles : l.q_tiles;
+        int4* out = ((i & 1) ? l.ktile : l.qtile) + (long long)z * cap;
         bool bad = false;
         int before = 0;
         for (int g0 = 0; g0 < G; g0 += 32) {
-            int n = 0;
+            int n = 0, lo = 0, hi = 0;
             if (g0 + lane < G) {
-                const int lo = off[g0 + lane], hi = off[g0 + lane + 1];
+                lo = off[g0 + lane];
+                hi = off[g0 + lane + 1];
                 if (lo < 0 || hi < lo || hi > N) bad = true;
                 else n = (hi - lo + kTile - 1) / kTile;
             }
@@ -111,10 +113,14 @@ __device__ void tile_lists(const ListParams& l, int wid, int lane) {
                 const int v = __shfl_up_sync(kFull, sum, o);
                 if (lane >= o) sum += v;
             }
-            if (g0 + lane < G) out[g0 + lane] = before + sum - n;
+            for (int t = 0; t < n; ++t) {
+                const int at = before + sum - n + t;
+                if (at < cap) out[at] = make_int4(g0 + lane, lo + t * kTile, min(kTile, hi - lo - t * kTile), 0);
+                else bad = true;       // more tiles than disjoint groups can have
+            }
             before += __shfl_sync(kFull, sum, 31);
         }
-        if (lane == 0) out[G] = before;
+        for (int t = before + lane; t < cap; t += 32) out[t] = make_int4(0, 0, 0, 0);
         if (__any_sync(kFull, bad) && lane == 0) set_status(status, kDevBounds);
         return;
     }
@@ -219,7 +225,8 @@ constexpr int kRegion = 16384;              // one [128 rows][64 bf16] region, 1
 constexpr int kThreads = 320;
 constexpr uint32_t kTmemCols = 512;
 
-// Set-up shared by the kernels: aligned shared memory, barriers (`count` arrivals each), TMEM.
+// Set-up shared by the kernels: aligned shared memory, barriers (`count` arrivals each), TMEM; the loading
+// warp starts on the tiles that stay (`early`) while the others set up.
 struct Cta {
     uint32_t base, bars, tmem;
     unsigned char* sbase;
@@ -228,8 +235,8 @@ struct Cta {
     __device__ __forceinline__ uint32_t bar(int i) const { return bars + 8u * (uint32_t)i; }
 };
 
-template <typename Count>
-__device__ __forceinline__ Cta cta_setup(unsigned char* smem_raw, int off_bar, int nbars, Count count) {
+template <typename Count, typename Early>
+__device__ __forceinline__ Cta cta_setup(unsigned char* smem_raw, int off_bar, int nbars, Count count, Early early) {
     Cta c;
     const uint32_t raw = tc::smem_addr(smem_raw);
     c.base = (raw + 1023u) & ~1023u;
@@ -239,10 +246,11 @@ __device__ __forceinline__ Cta cta_setup(unsigned char* smem_raw, int off_bar, i
     c.lane = threadIdx.x & 31;
     uint32_t* slot = reinterpret_cast<uint32_t*>(c.sbase + off_bar + 8 * nbars);
     c.abort_flag = reinterpret_cast<volatile int*>(slot + 1);
-    if (threadIdx.x == 0) {
+    if (c.warp == 8 && c.lane == 0) {
         for (int i = 0; i < nbars; ++i) tc::mbar_init(c.bar(i), count(i));
         *c.abort_flag = 0;
         tc::fence_mbar_init();
+        early(c);
     }
     if (c.warp == 9) {
         tc::tmem_alloc(tc::smem_addr(slot), kTmemCols);
@@ -466,22 +474,14 @@ __device__ __forceinline__ bf16* out_row(bf16* base, const int32_t* perm, long l
     return base + (head * N + row) * D;
 }
 
-// The tile of CTA `pair` on one side: rows [lo, lo + n) of group `grp`; false past the last tile.
-__device__ __forceinline__ bool find_tile(const int32_t* off, const int32_t* tile_off, int z, int G, int N, int pair,
-                                          int& grp, int& lo, int& n) {
-    grp = 0;
-    if (!off) {
-        lo = pair * kTile;
-        n = min(kTile, N - lo);
-        return true;
-    }
-    const int32_t* toff = tile_off + (long long)z * (G + 1);
-    if (pair >= toff[G]) return false;
-    grp = upper_index(toff, G, pair);
-    const int32_t* o = off + (long long)z * (G + 1);
-    lo = o[grp] + (pair - toff[grp]) * kTile;
-    n = min(kTile, o[grp + 1] - lo);
-    return true;
+// Tile `pair` of one side: rows [lo, lo + n) of group `grp`; false past the last tile. (A table: a
+// search of the group offsets costs a CTA some eight reads of memory one after another.)
+__device__ __forceinline__ bool find_tile(const int4* table, int z, int tiles, int N, int pair, int& grp, int& lo, int& n) {
+    const int4 e = table ? __ldg(table + (long long)z * tiles + pair) : make_int4(0, pair * kTile, min(kTile, N - pair * kTile), 0);
+    grp = e.x;
+    lo = e.y;
+    n = e.z;
+    return n > 0;
 }
 
 // ---------------------------------------------------------------- dK and dV
@@ -516,7 +516,7 @@ template <int D, bool PARTS>
 __device__ __forceinline__ void dkv_tile(const BwdMaps& m, const BwdParams& p, unsigned char* smem_raw, int z, int pair, int part) {
     using namespace kv;
     int grp, klo, kn;
-    if (!find_tile(p.koff, p.ktile_off, z, p.Gk, p.N, pair, grp, klo, kn)) return;
+    if (!find_tile(p.ktile, z, p.kv_tiles, p.N, pair, grp, klo, kn)) return;
     const int2* list = p.qlist + ((long long)z * p.Gk + grp) * p.qcap;
     const int nt = p.qcnt ? p.qcnt[(long long)z * p.Gk + grp] : (p.N + kTile - 1) / kTile;
     // this CTA's share of the (query head, query tile) stream
@@ -539,17 +539,17 @@ __device__ __forceinline__ void dkv_tile(const BwdMaps& m, const BwdParams& p, u
         }
         tc::fence_proxy_async_smem();
     }
-    const Cta c = cta_setup(smem_raw, kOffBar, kBars, [](int i) { return i >= kSread ? 256 : i >= kQf && i < kOf ? 2 : 1; });
-
-    if (c.warp == 8) {
-        if (c.lane == 0) {
+    const Cta c = cta_setup(
+        smem_raw, kOffBar, kBars, [](int i) { return i >= kSread ? 256 : i >= kQf && i < kOf ? 2 : 1; },
+        [&](const Cta& c) {
             tc::mbar_arrive_expect_tx(c.bar(kKV), 2 * (D / 64) * kRegion);
             for (int h = 0; h < D / 64; ++h) {
                 tc::tma_load_2d(c.base + kOffK + h * kRegion, &m.k, c.bar(kKV), 64 * h, z * p.N + klo);
                 tc::tma_load_2d(c.base + kOffV + h * kRegion, &m.v, c.bar(kKV), 64 * h, z * p.N + klo);
             }
-        }
-        __syncwarp();
+        });
+
+    if (c.warp == 8) {
         int nland = 0, nq = 0, no = 0, t = PARTS && nt ? first % nt : 0, x = z * p.g + (PARTS && nt ? first / nt : 0);
         // this lane's four rows of the next tile's terms; rows past its end give P = 2^(-huge) = 0
         float nl[4], nd[4];
@@ -745,7 +745,7 @@ __device__ __forceinline__ void dq_tile(const BwdMaps& m, const BwdParams& p, un
     using namespace dq;
     const int z = x / p.g;
     int grp, qlo, qn;
-    if (!find_tile(p.qoff, p.qtile_off, z, p.Gq, p.N, pair, grp, qlo, qn)) return;
+    if (!find_tile(p.qtile, z, p.q_tiles, p.N, pair, grp, qlo, qn)) return;
     const int2* list = p.klist + ((long long)z * p.Gq + grp) * p.kcap;
     // this CTA's share of the key tiles
     const int all = p.kcnt ? p.kcnt[(long long)z * p.Gq + grp] : (p.N + kTile - 1) / kTile;
@@ -755,17 +755,17 @@ __device__ __forceinline__ void dq_tile(const BwdMaps& m, const BwdParams& p, un
         t += first;
         return p.kcnt ? list[t] : make_int2(t * kTile, min(kTile, p.N - t * kTile));
     };
-    const Cta c = cta_setup(smem_raw, kOffBar, kBars, [](int i) { return i >= kSread ? 256 : 1; });
-
-    if (c.warp == 8) {
-        if (c.lane == 0) {
+    const Cta c = cta_setup(
+        smem_raw, kOffBar, kBars, [](int i) { return i >= kSread ? 256 : 1; },
+        [&](const Cta& c) {
             tc::mbar_arrive_expect_tx(c.bar(kQO), 2 * (D / 64) * kRegion);
             for (int h = 0; h < D / 64; ++h) {
                 tc::tma_load_2d(c.base + kOffQ + h * kRegion, &m.q, c.bar(kQO), 64 * h, x * p.N + qlo);
                 tc::tma_load_2d(c.base + kOffO + h * kRegion, &m.o, c.bar(kQO), 64 * h, x * p.N + qlo);
             }
-        }
-        __syncwarp();
+        });
+
+    if (c.warp == 8) {
         int nland = 0, nk = 0, nv = 0;
         for (int t = 0; t < nt; ++t) {
             const int2 e = tile(t);
@@ -948,7 +948,7 @@ size_t align256(size_t b) { return (b + 255) / 256 * 256; }
 
 // Byte offsets of the workspace's parts.
 struct BwdLayout {
-    size_t nlse2, nD, kv_part, q_part, klist, qlist, kcnt, qcnt, qtile_off, ktile_off, bytes;
+    size_t nlse2, nD, kv_part, q_part, klist, qlist, kcnt, qcnt, qtile, ktile, bytes;
     int kcap, qcap;
 };
 
@@ -974,8 +974,8 @@ BwdLayout bwd_layout(int P, int g, int N, int d, int Gq, int Gk, const BwdParts&
         l.qlist = take((size_t)P * Gk * l.qcap * sizeof(int2));
         l.kcnt = take((size_t)P * Gq * sizeof(int32_t));
         l.qcnt = take((size_t)P * Gk * sizeof(int32_t));
-        l.qtile_off = take((size_t)P * (Gq + 1) * sizeof(int32_t));
-        l.ktile_off = take((size_t)P * (Gk + 1) * sizeof(int32_t));
+        l.qtile = take((size_t)P * l.qcap * sizeof(int4));
+        l.ktile = take((size_t)P * l.kcap * sizeof(int4));
     }
     l.bytes = at;
     return l;
@@ -999,6 +999,9 @@ cudaError_t launch_bwd(const AttnBwdArgs& a, cudaStream_t s) {
     p.status = a.status;
     p.scale = (float)(1.0 / sqrt((double)D));
     p.scale_log2 = (float)(1.4426950408889634 / sqrt((double)D));
+    const int tiles = (a.N + kTile - 1) / kTile;
+    p.kv_tiles = tiles + (sparse ? a.Gk : 0);
+    p.q_tiles = tiles + (sparse ? a.Gq : 0);
     ListParams lp;
     memset(&lp, 0, sizeof(lp));
     int list_blocks = 0;
@@ -1006,14 +1009,15 @@ cudaError_t launch_bwd(const AttnBwdArgs& a, cudaStream_t s) {
         lp.rowptr = a.rowptr; lp.kg = a.kg; lp.qoff = a.qoff; lp.koff = a.koff;
         lp.klist = reinterpret_cast<int2*>(ws + l.klist); lp.qlist = reinterpret_cast<int2*>(ws + l.qlist);
         lp.kcnt = reinterpret_cast<int32_t*>(ws + l.kcnt); lp.qcnt = reinterpret_cast<int32_t*>(ws + l.qcnt);
-        lp.qtile_off = reinterpret_cast<int32_t*>(ws + l.qtile_off);
-        lp.ktile_off = reinterpret_cast<int32_t*>(ws + l.ktile_off);
+        lp.qtile = reinterpret_cast<int4*>(ws + l.qtile);
+        lp.ktile = reinterpret_cast<int4*>(ws + l.ktile);
+        lp.q_tiles = p.q_tiles; lp.kv_tiles = p.kv_tiles;
         lp.status = a.status;
         lp.kcap = l.kcap; lp.qcap = l.qcap; lp.P = a.P; lp.N = a.N; lp.Gq = a.Gq; lp.Gk = a.Gk;
         list_blocks = (int)(((long long)a.P * (a.Gq + a.Gk + 2) * 32 + 255) / 256);
-        p.qoff = a.qoff; p.koff = a.koff; p.qperm = a.qperm; p.kperm = a.kperm;
+        p.qperm = a.qperm; p.kperm = a.kperm;
         p.klist = lp.klist; p.qlist = lp.qlist; p.kcnt = lp.kcnt; p.qcnt = lp.qcnt;
-        p.qtile_off = lp.qtile_off; p.ktile_off = lp.ktile_off;
+        p.qtile = lp.qtile; p.ktile = lp.ktile;
         p.kcap = l.kcap; p.qcap = l.qcap;
         p.Gq = a.Gq; p.Gk = a.Gk;
     }
@@ -1026,9 +1030,6 @@ cudaError_t launch_bwd(const AttnBwdArgs& a, cudaStream_t s) {
     if (!make_tmap_bf16_sw128(&m.q, a.Q, rows, D, kTile, 64) || !make_tmap_bf16_sw128(&m.k, a.K, krows, D, kTile, 64) ||
         !make_tmap_bf16_sw128(&m.v, a.V, krows, D, kTile, 64) || !make_tmap_bf16_sw128(&m.o, a.dO, rows, D, kTile, 64))
         return cudaErrorInvalidValue;
-    const int tiles = (a.N + kTile - 1) / kTile;
-    p.kv_tiles = tiles + (sparse ? a.Gk : 0);
-    p.q_tiles = tiles + (sparse ? a.Gq : 0);
     p.kv_blocks = a.dK ? p.kv_tiles * a.P * p.kv_parts : 0;
     const long long blocks = p.kv_blocks + (a.dQ ? (long long)p.q_tiles * a.P * a.g * p.q_parts : 0);
     const bool parts = p.kv_parts > 1 || p.q_parts > 1;
