@@ -212,9 +212,9 @@ __global__ void __launch_bounds__(256) bwd_prepare_kernel(const ListParams l, in
 }
 
 // ---------------------------------------------------------------- gradients
-// Both kernels run ten warps: two warpgroups that form P and dS (thread r of warpgroup w owns TMEM
-// lane r of columns 64 w .. 64 w + 63), warp 8 loads tiles (TMA), warp 9 allocates TMEM and issues
-// every MMA. P and dS go back to TMEM as bf16 pairs, where they are the A operands of the next
+// Both kernels run two or four warpgroups that form P and dS (thread r of a warpgroup owns TMEM lane r of
+// the warpgroup's share of the 128 columns), a warp that loads tiles (TMA) and one that allocates TMEM and
+// issues every MMA. P and dS go back to TMEM as bf16 pairs, where they are the A operands of the next
 // product, so no transposed copy is ever made: the dK/dV kernel keeps keys in the lanes
 // (S^T = K Q^T), the dQ kernel queries. They have columns of their own, so the fp32 columns of S and
 // dP are free again as soon as they have been read, and the next product into them runs beside the
@@ -222,7 +222,15 @@ __global__ void __launch_bounds__(256) bwd_prepare_kernel(const ListParams l, in
 // Rows of a streamed tile past its valid ones belong to another group or head: the loading warp
 // zeroes them in shared memory, so that no value there, finite or not, reaches a sum.
 constexpr int kRegion = 16384;              // one [128 rows][64 bf16] region, 128-byte swizzle
-constexpr int kThreads = 320;
+// Warpgroups that form P and dS, and the warps after them. d = 64 halves the products' time but not the
+// arithmetic's, so it takes four where d = 128 takes two (24 heads x 4096 rows, d = 64: 433 us with two, 416
+// with four; 12 heads, d = 128: 278 and 280).
+template <int D>
+struct Warps {
+    static constexpr int kWgs = D == 64 ? 4 : 2, kTma = 4 * kWgs, kMma = kTma + 1, kThreads = 32 * (kMma + 1);
+    static constexpr int kArrivals = 128 * kWgs;
+    static constexpr int kCols = kTile / kWgs, kH = kCols / 32;     // columns of a thread, in blocks of 32
+};
 constexpr uint32_t kTmemCols = 512;
 
 // Set-up shared by the kernels: aligned shared memory, barriers (`count` arrivals each), TMEM; the loading
@@ -231,11 +239,11 @@ struct Cta {
     uint32_t base, bars, tmem;
     unsigned char* sbase;
     volatile int* abort_flag;
-    int warp, lane;
+    int warp, lane, mma_warp;
     __device__ __forceinline__ uint32_t bar(int i) const { return bars + 8u * (uint32_t)i; }
 };
 
-template <typename Count, typename Early>
+template <int D, typename Count, typename Early>
 __device__ __forceinline__ Cta cta_setup(unsigned char* smem_raw, int off_bar, int nbars, Count count, Early early) {
     Cta c;
     const uint32_t raw = tc::smem_addr(smem_raw);
@@ -244,15 +252,16 @@ __device__ __forceinline__ Cta cta_setup(unsigned char* smem_raw, int off_bar, i
     c.bars = c.base + off_bar;
     c.warp = threadIdx.x >> 5;
     c.lane = threadIdx.x & 31;
+    c.mma_warp = Warps<D>::kMma;
     uint32_t* slot = reinterpret_cast<uint32_t*>(c.sbase + off_bar + 8 * nbars);
     c.abort_flag = reinterpret_cast<volatile int*>(slot + 1);
-    if (c.warp == 8 && c.lane == 0) {
+    if (c.warp == Warps<D>::kTma && c.lane == 0) {
         for (int i = 0; i < nbars; ++i) tc::mbar_init(c.bar(i), count(i));
         *c.abort_flag = 0;
         tc::fence_mbar_init();
         early(c);
     }
-    if (c.warp == 9) {
+    if (c.warp == Warps<D>::kMma) {
         tc::tmem_alloc(tc::smem_addr(slot), kTmemCols);
         tc::tmem_relinquish();
     }
@@ -268,7 +277,7 @@ __device__ __forceinline__ void cta_finish(const Cta& c, int* status) {
     tc::fence_before_sync();
     __syncthreads();
     if (threadIdx.x == 0 && *c.abort_flag) set_status(status, kDevTimeout);
-    if (c.warp == 9) {
+    if (c.warp == c.mma_warp) {
         tc::fence_after_sync();
         tc::tmem_dealloc(c.tmem, kTmemCols);
     }
@@ -418,6 +427,17 @@ __device__ __forceinline__ void ex2_pair(uint64_t x2, int i, uint32_t& a, uint32
     b = __float_as_uint(x1);
 }
 
+// This thread's 32 kH columns of an fp32 tile.
+template <int kH>
+__device__ __forceinline__ void load_cols(uint32_t taddr, uint32_t (&v)[kH][32]) {
+    static_assert(kH == 1 || kH == 2, "blocks of 32 columns");
+    tc::tmem_ld32(taddr, v[0]);
+    if (kH == 2) tc::tmem_ld32(taddr + 32, v[kH - 1]);
+    tc::tmem_wait_ld();
+    tc::regs_after_wait(v[0]);
+    if (kH == 2) tc::regs_after_wait(v[kH - 1]);
+}
+
 // One fp32 accumulator row of D TMEM columns, times `scale`, rounded to bf16 into `out`.
 template <int D>
 __device__ __forceinline__ void store_acc_row(uint32_t tacc, float scale, bf16* out, bool zero) {
@@ -488,33 +508,52 @@ __device__ __forceinline__ bool find_tile(const int4* table, int z, int tiles, i
 // One CTA per 128-key tile, streaming the (Q, dO) tiles of every query head of the KV head and
 // every query tile that keeps the key group. Per tile, with keys in the TMEM lanes:
 //   S^T = K Q^T -> P^T;  dV += P^T dO;  dP^T = V dO^T -> dS^T;  dK += dS^T Q.
-// dV and dK take 256 of the 512 TMEM columns, P and dS 64 each; S and dP share the other 128 in
+// At d = 128, dV and dK take 256 of the 512 TMEM columns, P and dS 64 each; S and dP share the other 128 in
 // turn: dP(i) is issued when S(i) has been read, S(i+1) when dP(i) has. Issue order dP(i),
 // dK(i-1), S(i+1), dV(i): dP and dK run beside the exponentials, S and dV beside dS.
 // The terms -lse and -D of a query vary along the columns here, so a thread would need every query's:
 // they are added by the products instead. One more K step of 16 multiplies ones on the key side with
 // the three bf16 parts (24 bits) of -lse sqrt(d), or of -D, on the query side.
-// Four 128-row buffers hold the streamed tiles. dO(i) is done with a product before Q(i), and Q(i+2)
+// At d = 64 S and dP have columns of their own: S(i+1) follows the reading of S(i), dP(i+1) that of dP(i).
+// At d = 128 four 128-row buffers hold the streamed tiles. dO(i) is done with a product before Q(i), and Q(i+2)
 // is wanted before dO(i+2): Q(i+2) takes the buffer of dO(i), dO(i+2) that of Q(i).
 namespace kv {
-constexpr int kStages = 2;
-constexpr int kOffK = 0, kOffV = 2 * kRegion, kOffBuf = 4 * kRegion, kOffExt = kOffBuf + 2 * kStages * 2 * kRegion,
-              kOffOne = kOffExt + kStages * kExtBytes, kOffBar = kOffOne + 2 * kExtBytes;
-// Buffers of tile i: stage i % 2 has two, which Q and dO swap from one use of the stage to the next.
-__device__ __forceinline__ int buf_q(int i) { return kOffBuf + (2 * (i & 1) + ((i >> 1) & 1)) * 2 * kRegion; }
-__device__ __forceinline__ int buf_o(int i) { return kOffBuf + (2 * (i & 1) + (((i >> 1) & 1) ^ 1)) * 2 * kRegion; }
-// full / empty stages (Q's full one also stands for the row terms); S and dP ready, read; P and dS written;
-// all MMAs done; ragged loads
-enum { kKV = 0, kQf = 1, kOf = kQf + kStages, kQe = kOf + kStages, kOe = kQe + kStages, kS = kOe + kStages, kDP, kDone, kLand,
-       kSread, kDPread, kP, kDS, kBars };
-constexpr int kSmem = kOffBar + 8 * kBars + 16 + 1024;
-static_assert(kSmem <= 232448, "shared memory budget");
-constexpr uint32_t kTS = 0, kTP = 128, kTDS = 192, kTDV = 256, kTDK = 384;      // dP: the columns of S
+constexpr int kOffK = 0, kOffV = 2 * kRegion, kOffBuf = 4 * kRegion;
+constexpr int kKV = 0, kQf = 1;             // the first barriers
+constexpr uint32_t kTS = 0;
+// What depends on d: d = 128 has two stages of Q and dO and S and dP in the same columns, d = 64 (tiles of
+// half the size, sums of half the columns) four stages and columns of their own.
+template <int D>
+struct Layout {
+    static constexpr int kStages = D == 64 ? 4 : 2;
+    static constexpr int kOffExt = kOffBuf + 8 * kRegion, kOffOne = kOffExt + kStages * kExtBytes, kOffBar = kOffOne + 2 * kExtBytes;
+    // full / empty stages (Q's full one also stands for the row terms); S and dP ready, read; P and dS written;
+    // all MMAs done; ragged loads
+    enum { kOf = kQf + kStages, kQe = kOf + kStages, kOe = kQe + kStages, kS = kOe + kStages, kDP, kDone, kLand, kSread, kDPread,
+           kP, kDS, kBars };
+    static constexpr int kSmem = kOffBar + 8 * kBars + 16 + 1024;
+    static constexpr uint32_t kTDP = D == 64 ? 128 : 0, kTP = D == 64 ? 256 : 128, kTDS = kTP + 64, kTDV = D == 64 ? 384 : 256,
+                              kTDK = kTDV + D;
+    static_assert(kSmem <= 232448 && kTDK + D <= kTmemCols, "shared memory or TMEM budget");
+    // Buffers of tile i. d = 128: stage i % 2 has two, which Q and dO swap from one use of the stage to the next.
+    static __device__ __forceinline__ int q(int i) {
+        return kOffBuf + (D == 64 ? (i & 3) * kRegion : (2 * (i & 1) + ((i >> 1) & 1)) * 2 * kRegion);
+    }
+    static __device__ __forceinline__ int o(int i) {
+        return kOffBuf + (D == 64 ? (4 + (i & 3)) * kRegion : (2 * (i & 1) + (((i >> 1) & 1) ^ 1)) * 2 * kRegion);
+    }
+};
 }  // namespace kv
 
 template <int D, bool PARTS>
 __device__ __forceinline__ void dkv_tile(const BwdMaps& m, const BwdParams& p, unsigned char* smem_raw, int z, int pair, int part) {
     using namespace kv;
+    using W = Warps<D>;
+    using L = Layout<D>;
+    constexpr int kStages = L::kStages, kTP = L::kTP, kTDS = L::kTDS, kTDV = L::kTDV, kTDK = L::kTDK;
+    constexpr int kOffExt = L::kOffExt, kOffOne = L::kOffOne, kOffBar = L::kOffBar;
+    constexpr int kOf = L::kOf, kQe = L::kQe, kOe = L::kOe, kS = L::kS, kDP = L::kDP, kDone = L::kDone, kLand = L::kLand, kSread = L::kSread,
+                  kDPread = L::kDPread, kP = L::kP, kDS = L::kDS, kBars = L::kBars;
     int grp, klo, kn;
     if (!find_tile(p.ktile, z, p.kv_tiles, p.N, pair, grp, klo, kn)) return;
     const int2* list = p.qlist + ((long long)z * p.Gk + grp) * p.qcap;
@@ -530,7 +569,7 @@ __device__ __forceinline__ void dkv_tile(const BwdMaps& m, const BwdParams& p, u
         const uint32_t off = ((tc::smem_addr(smem_raw) + 1023u) & ~1023u) - tc::smem_addr(smem_raw);
         uint4* ext = reinterpret_cast<uint4*>(smem_raw + off + kOffExt);
         constexpr uint32_t one = 0x3f80u;
-        for (int i = threadIdx.x; i < (kStages + 2) * 2 * kTile; i += kThreads) {
+        for (int i = threadIdx.x; i < (kStages + 2) * 2 * kTile; i += W::kThreads) {
             const int t = i / (2 * kTile);
             uint4 v = make_uint4(0, 0, 0, 0);
             if (i % (2 * kTile) < kTile && t == kStages) v = make_uint4(one | one << 16, one, 0, 0);
@@ -539,8 +578,8 @@ __device__ __forceinline__ void dkv_tile(const BwdMaps& m, const BwdParams& p, u
         }
         tc::fence_proxy_async_smem();
     }
-    const Cta c = cta_setup(
-        smem_raw, kOffBar, kBars, [](int i) { return i >= kSread ? 256 : i >= kQf && i < kOf ? 2 : 1; },
+    const Cta c = cta_setup<D>(
+        smem_raw, kOffBar, kBars, [](int i) { return i >= kSread ? W::kArrivals : i >= kQf && i < kOf ? 2 : 1; },
         [&](const Cta& c) {
             tc::mbar_arrive_expect_tx(c.bar(kKV), 2 * (D / 64) * kRegion);
             for (int h = 0; h < D / 64; ++h) {
@@ -549,7 +588,7 @@ __device__ __forceinline__ void dkv_tile(const BwdMaps& m, const BwdParams& p, u
             }
         });
 
-    if (c.warp == 8) {
+    if (c.warp == W::kTma) {
         int nland = 0, nq = 0, no = 0, t = PARTS && nt ? first % nt : 0, x = z * p.g + (PARTS && nt ? first / nt : 0);
         // this lane's four rows of the next tile's terms; rows past its end give P = 2^(-huge) = 0
         float nl[4], nd[4];
@@ -572,9 +611,9 @@ __device__ __forceinline__ void dkv_tile(const BwdMaps& m, const BwdParams& p, u
                 ++x;
             }
             const int2 next = it + 1 < iters ? tile(t) : make_int2(0, 0);
-            // Q(it) follows dO(it - 2) in its buffer, dO(it) follows Q(it - 2)
-            if (it >= kStages && !__all_sync(kFull, tc::mbar_wait(c.bar(kOe + s), (it / kStages - 1) & 1, c.abort_flag))) break;
-            if (!load_tile_zeroed<D>(c, c.base + buf_q(it), &m.q, kQf + s, kLand, nland, row, valid)) break;
+            // d = 128: Q(it) follows dO(it - 2) in its buffer, dO(it) follows Q(it - 2)
+            if (it >= kStages && !__all_sync(kFull, tc::mbar_wait(c.bar((D == 64 ? kQe : kOe) + s), (it / kStages - 1) & 1, c.abort_flag))) break;
+            if (!load_tile_zeroed<D>(c, c.base + L::q(it), &m.q, kQf + s, kLand, nland, row, valid)) break;
             nq = it + 1;
             uint4* ext = reinterpret_cast<uint4*>(c.sbase + kOffExt + s * kExtBytes);
 #pragma unroll
@@ -590,8 +629,9 @@ __device__ __forceinline__ void dkv_tile(const BwdMaps& m, const BwdParams& p, u
             __syncwarp();
             if (c.lane == 0) tc::mbar_arrive(c.bar(kQf + s));
             if (it + 1 < iters) fetch(next, x);
-            if (it >= kStages && !__all_sync(kFull, tc::mbar_wait(c.bar(kQe + s), (it / kStages - 1) & 1, c.abort_flag))) break;
-            if (!load_tile_zeroed<D>(c, c.base + buf_o(it), &m.o, kOf + s, kLand, nland, row, valid)) break;
+            if (it >= kStages && !__all_sync(kFull, tc::mbar_wait(c.bar((D == 64 ? kOe : kQe) + s), (it / kStages - 1) & 1, c.abort_flag)))
+                break;
+            if (!load_tile_zeroed<D>(c, c.base + L::o(it), &m.o, kOf + s, kLand, nland, row, valid)) break;
             no = it + 1;
             e = next;
         }
@@ -600,16 +640,16 @@ __device__ __forceinline__ void dkv_tile(const BwdMaps& m, const BwdParams& p, u
         for (int i = max(0, nq - kStages); i < nq; ++i) tc::mbar_wait(c.bar(kQf + i % kStages), (i / kStages) & 1, &never);
         for (int i = max(0, no - kStages); i < no; ++i) tc::mbar_wait(c.bar(kOf + i % kStages), (i / kStages) & 1, &never);
         tc::mbar_wait(c.bar(kKV), 0, &never);
-    } else if (c.warp == 9) {
+    } else if (c.warp == W::kMma) {
         const uint32_t go = tc::elect_one();
         auto wait = [&](int b, int parity) {
             const bool ok = __all_sync(kFull, tc::mbar_wait(c.bar(b), parity & 1, c.abort_flag));
             tc::fence_after_sync();
             return ok;
         };
-        const uint32_t tS = c.tmem + kTS;
-        auto q = [&](int it) { return c.base + buf_q(it); };
-        auto o = [&](int it) { return c.base + buf_o(it); };
+        const uint32_t tS = c.tmem + kTS, tDP = c.tmem + L::kTDP;
+        auto q = [&](int it) { return c.base + L::q(it); };
+        auto o = [&](int it) { return c.base + L::o(it); };
         auto ext = [&](int it) { return c.base + kOffExt + (it % kStages) * kExtBytes; };
         auto issue_S = [&](int it) {
             mma_rows<D>(tS, c.base + kOffK, q(it), go);
@@ -624,20 +664,35 @@ __device__ __forceinline__ void dkv_tile(const BwdMaps& m, const BwdParams& p, u
         };
         bool ok = iters > 0 && wait(kKV, 0) && wait(kQf, 0);
         if (ok) issue_S(0);
-        for (int it = 0; ok && it < iters; ++it) {
-            if (!wait(kOf + it % kStages, it / kStages) || !wait(kSread, it)) break;
-            mma_rows<D>(tS, c.base + kOffV, o(it), go);
-            mma_ext(tS, c.base + kOffOne + kExtBytes, ext(it), go);
+        auto issue_dP = [&](int it) {
+            mma_rows<D>(tDP, c.base + kOffV, o(it), go);
+            mma_ext(tDP, c.base + kOffOne + kExtBytes, ext(it), go);
             tc::commit_go(c.bar(kDP), go);
-            if (it > 0 && !issue_dK(it - 1)) break;
-            if (it + 1 < iters) {
-                if (!wait(kQf + (it + 1) % kStages, (it + 1) / kStages) || !wait(kDPread, it)) break;
-                issue_S(it + 1);
+        };
+        for (int it = 0; ok && it < iters; ++it) {
+            const bool more = it + 1 < iters;
+            if (!wait(kOf + it % kStages, it / kStages)) break;
+            if (D == 64) {
+                if (it > 0 && !wait(kDPread, it - 1)) break;
+                issue_dP(it);
+                if (more) {
+                    if (!wait(kQf + (it + 1) % kStages, (it + 1) / kStages) || !wait(kSread, it)) break;
+                    issue_S(it + 1);
+                }
+                if (it > 0 && !issue_dK(it - 1)) break;
+            } else {
+                if (!wait(kSread, it)) break;
+                issue_dP(it);
+                if (it > 0 && !issue_dK(it - 1)) break;
+                if (more) {
+                    if (!wait(kQf + (it + 1) % kStages, (it + 1) / kStages) || !wait(kDPread, it)) break;
+                    issue_S(it + 1);
+                }
             }
             if (!wait(kP, it)) break;
             mma_sums<D>(c.tmem + kTDV, c.tmem + kTP, o(it), it > 0, go);
             tc::commit_go(c.bar(kOe + it % kStages), go);
-            if (it + 1 == iters) issue_dK(it);
+            if (!more) issue_dK(it);
         }
         // every issued MMA completes before the sums are read and TMEM is released
         tc::commit_go(c.bar(kDone), go);
@@ -646,23 +701,19 @@ __device__ __forceinline__ void dkv_tile(const BwdMaps& m, const BwdParams& p, u
     } else {
         const int w = c.warp >> 2, r = threadIdx.x & 127;
         const uint32_t lane_off = (uint32_t)((c.warp & 3) * 32) << 16;
-        const uint32_t tS = c.tmem + kTS + 64 * w + lane_off;
-        const uint32_t tP = c.tmem + kTP + 32 * w + lane_off, tDS = c.tmem + kTDS + 32 * w + lane_off;
+        const uint32_t tS = c.tmem + kTS + W::kCols * w + lane_off, tDP = c.tmem + L::kTDP + W::kCols * w + lane_off;
+        const uint32_t tP = c.tmem + kTP + W::kCols / 2 * w + lane_off, tDS = c.tmem + kTDS + W::kCols / 2 * w + lane_off;
         const uint64_t cc = pk2(p.scale_log2, p.scale_log2);
         bool ok = true;
         for (int it = 0; it < iters; ++it) {
             if (!__all_sync(kFull, tc::mbar_wait(c.bar(kS), it & 1, c.abort_flag))) { ok = false; break; }
             tc::fence_after_sync();
-            uint32_t pv[2][32];
-            tc::tmem_ld32(tS, pv[0]);
-            tc::tmem_ld32(tS + 32, pv[1]);
-            tc::tmem_wait_ld();
-            tc::regs_after_wait(pv[0]);
-            tc::regs_after_wait(pv[1]);
+            uint32_t pv[W::kH][32];
+            load_cols(tS, pv);
             tc::fence_before_sync();
             tc::mbar_arrive(c.bar(kSread));
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+            for (int h = 0; h < W::kH; ++h)
 #pragma unroll
                 for (int i = 0; i < 32; i += 2)
                     ex2_pair(mul2(pk2(__uint_as_float(pv[h][i]), __uint_as_float(pv[h][i + 1])), cc), i / 2, pv[h][i],
@@ -672,7 +723,7 @@ __device__ __forceinline__ void dkv_tile(const BwdMaps& m, const BwdParams& p, u
             if (it > 0 && !__all_sync(kFull, tc::mbar_wait(c.bar(kOe + prev), phase, c.abort_flag))) { ok = false; break; }
             tc::fence_after_sync();
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
+            for (int h = 0; h < W::kH; ++h) {
                 uint32_t pk[16];
 #pragma unroll
                 for (int e = 0; e < 16; ++e) pk[e] = bf16x2(__uint_as_float(pv[h][2 * e]), __uint_as_float(pv[h][2 * e + 1]));
@@ -683,16 +734,12 @@ __device__ __forceinline__ void dkv_tile(const BwdMaps& m, const BwdParams& p, u
             tc::mbar_arrive(c.bar(kP));
             if (!__all_sync(kFull, tc::mbar_wait(c.bar(kDP), it & 1, c.abort_flag))) { ok = false; break; }
             tc::fence_after_sync();
-            uint32_t dv[2][32];
-            tc::tmem_ld32(tS, dv[0]);
-            tc::tmem_ld32(tS + 32, dv[1]);
-            tc::tmem_wait_ld();
-            tc::regs_after_wait(dv[0]);
-            tc::regs_after_wait(dv[1]);
+            uint32_t dv[W::kH][32];
+            load_cols(tDP, dv);
             tc::fence_before_sync();
             tc::mbar_arrive(c.bar(kDPread));
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+            for (int h = 0; h < W::kH; ++h)
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
                     float x0, x1;
@@ -703,22 +750,24 @@ __device__ __forceinline__ void dkv_tile(const BwdMaps& m, const BwdParams& p, u
                 }
             if (it > 0 && !__all_sync(kFull, tc::mbar_wait(c.bar(kQe + prev), phase, c.abort_flag))) { ok = false; break; }
             tc::fence_after_sync();
-            tc::tmem_st16(tDS, pv[0]);
-            tc::tmem_st16(tDS + 16, pv[1]);
+#pragma unroll
+            for (int h = 0; h < W::kH; ++h) tc::tmem_st16(tDS + 16 * h, pv[h]);
             tc::tmem_wait_st();
             tc::fence_before_sync();
             tc::mbar_arrive(c.bar(kDS));
         }
-        // warpgroup 0 stores dV, warpgroup 1 dK
+        // even warpgroups store dV, odd ones dK, each its share of the row's columns
         if (__all_sync(kFull, ok && tc::mbar_wait(c.bar(kDone), 0, c.abort_flag))) {
             tc::fence_after_sync();
-            const uint32_t acc = c.tmem + (w ? kTDK : kTDV) + lane_off;
+            constexpr int kN = D / (W::kWgs / 2);
+            const int is_dk = w & 1, col = (w >> 1) * kN;
+            const uint32_t acc = c.tmem + (is_dk ? kTDK : kTDV) + col + lane_off;
             if (PARTS && p.kv_parts > 1) {
-                const long long row = (part * 2 + w) * p.krows + (long long)z * p.N + klo + r;
-                store_part_row<D>(acc, r < kn ? p.kv_part + row * D : nullptr, iters == 0);
+                const long long row = (part * 2 + is_dk) * p.krows + (long long)z * p.N + klo + r;
+                store_part_row<kN>(acc, r < kn ? p.kv_part + row * D + col : nullptr, iters == 0);
             } else {
-                bf16* out = out_row<D>(w ? p.dK : p.dV, p.kperm, z, p.N, klo + r, r < kn, z, p.status);
-                store_acc_row<D>(acc, w ? p.scale : 1.f, out, iters == 0);
+                bf16* out = out_row<D>(is_dk ? p.dK : p.dV, p.kperm, z, p.N, klo + r, r < kn, z, p.status);
+                store_acc_row<kN>(acc, is_dk ? p.scale : 1.f, out ? out + col : nullptr, iters == 0);
             }
         }
     }
@@ -743,6 +792,7 @@ constexpr uint32_t kTS = 0, kTDP = 128, kTDQ = 256, kTDS = 384;
 template <int D, bool PARTS>
 __device__ __forceinline__ void dq_tile(const BwdMaps& m, const BwdParams& p, unsigned char* smem_raw, int x, int pair, int part) {
     using namespace dq;
+    using W = Warps<D>;
     const int z = x / p.g;
     int grp, qlo, qn;
     if (!find_tile(p.qtile, z, p.q_tiles, p.N, pair, grp, qlo, qn)) return;
@@ -755,8 +805,8 @@ __device__ __forceinline__ void dq_tile(const BwdMaps& m, const BwdParams& p, un
         t += first;
         return p.kcnt ? list[t] : make_int2(t * kTile, min(kTile, p.N - t * kTile));
     };
-    const Cta c = cta_setup(
-        smem_raw, kOffBar, kBars, [](int i) { return i >= kSread ? 256 : 1; },
+    const Cta c = cta_setup<D>(
+        smem_raw, kOffBar, kBars, [](int i) { return i >= kSread ? W::kArrivals : 1; },
         [&](const Cta& c) {
             tc::mbar_arrive_expect_tx(c.bar(kQO), 2 * (D / 64) * kRegion);
             for (int h = 0; h < D / 64; ++h) {
@@ -765,7 +815,7 @@ __device__ __forceinline__ void dq_tile(const BwdMaps& m, const BwdParams& p, un
             }
         });
 
-    if (c.warp == 8) {
+    if (c.warp == W::kTma) {
         int nland = 0, nk = 0, nv = 0;
         for (int t = 0; t < nt; ++t) {
             const int2 e = tile(t);
@@ -781,7 +831,7 @@ __device__ __forceinline__ void dq_tile(const BwdMaps& m, const BwdParams& p, un
         for (int i = max(0, nk - kKStages); i < nk; ++i) tc::mbar_wait(c.bar(kKf + i % kKStages), (i / kKStages) & 1, &never);
         for (int i = max(0, nv - kVStages); i < nv; ++i) tc::mbar_wait(c.bar(kVf + i % kVStages), (i / kVStages) & 1, &never);
         tc::mbar_wait(c.bar(kQO), 0, &never);
-    } else if (c.warp == 9) {
+    } else if (c.warp == W::kMma) {
         const uint32_t go = tc::elect_one();
         auto wait = [&](int b, int parity) {
             const bool ok = __all_sync(kFull, tc::mbar_wait(c.bar(b), parity & 1, c.abort_flag));
@@ -817,8 +867,8 @@ __device__ __forceinline__ void dq_tile(const BwdMaps& m, const BwdParams& p, un
     } else {
         const int w = c.warp >> 2, r = threadIdx.x & 127;
         const uint32_t lane_off = (uint32_t)((c.warp & 3) * 32) << 16;
-        const uint32_t tS = c.tmem + kTS + 64 * w + lane_off, tDP = c.tmem + kTDP + 64 * w + lane_off;
-        const uint32_t tDS = c.tmem + kTDS + 32 * w + lane_off;
+        const uint32_t tS = c.tmem + kTS + W::kCols * w + lane_off, tDP = c.tmem + kTDP + W::kCols * w + lane_off;
+        const uint32_t tDS = c.tmem + kTDS + W::kCols / 2 * w + lane_off;
         const long long row = (long long)x * p.N + qlo + r;
         const float nl = r < qn ? p.nlse2[row] : -INFINITY, nd = r < qn ? p.nD[row] : 0.f;
         const uint64_t cc = pk2(p.scale_log2, p.scale_log2), nl2 = pk2(nl, nl), nd2 = pk2(nd, nd);
@@ -829,16 +879,12 @@ __device__ __forceinline__ void dq_tile(const BwdMaps& m, const BwdParams& p, un
             if (t + 1 < nt) valid_next = tile(t + 1).y;
             if (!__all_sync(kFull, tc::mbar_wait(c.bar(kS), t & 1, c.abort_flag))) { ok = false; break; }
             tc::fence_after_sync();
-            uint32_t pv[2][32], pk[32];
-            tc::tmem_ld32(tS, pv[0]);
-            tc::tmem_ld32(tS + 32, pv[1]);
-            tc::tmem_wait_ld();
-            tc::regs_after_wait(pv[0]);
-            tc::regs_after_wait(pv[1]);
+            uint32_t pv[W::kH][32], pk[16 * W::kH];
+            load_cols(tS, pv);
             tc::fence_before_sync();
             tc::mbar_arrive(c.bar(kSread));
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
+            for (int h = 0; h < W::kH; ++h) {
 #pragma unroll
                 for (int i = 0; i < 32; i += 2)
                     ex2_pair(fma2(pk2(__uint_as_float(pv[h][i]), __uint_as_float(pv[h][i + 1])), cc, nl2), i / 2, pv[h][i],
@@ -846,21 +892,17 @@ __device__ __forceinline__ void dq_tile(const BwdMaps& m, const BwdParams& p, un
                 if (valid < kTile) {      // keys past the tile's end
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
-                        if (64 * w + 32 * h + i >= valid) pv[h][i] = 0u;
+                        if (W::kCols * w + 32 * h + i >= valid) pv[h][i] = 0u;
                 }
             }
             if (!__all_sync(kFull, tc::mbar_wait(c.bar(kDP), t & 1, c.abort_flag))) { ok = false; break; }
             tc::fence_after_sync();
-            uint32_t dv[2][32];
-            tc::tmem_ld32(tDP, dv[0]);
-            tc::tmem_ld32(tDP + 32, dv[1]);
-            tc::tmem_wait_ld();
-            tc::regs_after_wait(dv[0]);
-            tc::regs_after_wait(dv[1]);
+            uint32_t dv[W::kH][32];
+            load_cols(tDP, dv);
             tc::fence_before_sync();
             tc::mbar_arrive(c.bar(kDPread));
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
+            for (int h = 0; h < W::kH; ++h) {
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
                     float x0, x1;
@@ -872,21 +914,23 @@ __device__ __forceinline__ void dq_tile(const BwdMaps& m, const BwdParams& p, un
             }
             if (t > 0 && !__all_sync(kFull, tc::mbar_wait(c.bar(kDSfree), (t - 1) & 1, c.abort_flag))) { ok = false; break; }
             tc::fence_after_sync();
-            tc::tmem_st32(tDS, pk);
+            if (W::kH == 2) tc::tmem_st32(tDS, pk);
+            else tc::tmem_st16(tDS, pk);
             tc::tmem_wait_st();
             tc::fence_before_sync();
             tc::mbar_arrive(c.bar(kDS));
         }
-        if (__all_sync(kFull, ok && tc::mbar_wait(c.bar(kDone), 0, c.abort_flag))) {
+        // the first two warpgroups store half of the row's columns each
+        constexpr int kN = D / 2;
+        if (w < 2 && __all_sync(kFull, ok && tc::mbar_wait(c.bar(kDone), 0, c.abort_flag))) {
             tc::fence_after_sync();
-            // each warpgroup stores half of the row's columns
-            const uint32_t acc = c.tmem + kTDQ + w * (D / 2) + lane_off;
+            const uint32_t acc = c.tmem + kTDQ + w * kN + lane_off;
             if (PARTS && p.q_parts > 1) {
-                float* out = p.q_part + (part * p.qrows + (long long)x * p.N + qlo + r) * D + w * (D / 2);
-                store_part_row<D / 2>(acc, r < qn ? out : nullptr, nt == 0);
+                float* out = p.q_part + (part * p.qrows + (long long)x * p.N + qlo + r) * D + w * kN;
+                store_part_row<kN>(acc, r < qn ? out : nullptr, nt == 0);
             } else {
                 bf16* out = out_row<D>(p.dQ, p.qperm, x, p.N, qlo + r, r < qn, z, p.status);
-                store_acc_row<D / 2>(acc, p.scale, out ? out + w * (D / 2) : nullptr, nt == 0);
+                store_acc_row<kN>(acc, p.scale, out ? out + w * kN : nullptr, nt == 0);
             }
         }
     }
@@ -895,10 +939,11 @@ __device__ __forceinline__ void dq_tile(const BwdMaps& m, const BwdParams& p, un
 
 // Both passes in one launch: the CTAs of dK and dV come first, being the longer ones, and those of dQ
 // fill the SMs that they leave idle at their end.
-constexpr int kSmemBytes = kv::kSmem > dq::kSmem ? kv::kSmem : dq::kSmem;
+template <int D>
+constexpr int kSmemBytes = kv::Layout<D>::kSmem > dq::kSmem ? kv::Layout<D>::kSmem : dq::kSmem;
 
 template <int D, bool PARTS>
-__global__ void __launch_bounds__(kThreads, 1) bwd_kernel(const __grid_constant__ BwdMaps m, const __grid_constant__ BwdParams p) {
+__global__ void __launch_bounds__(Warps<D>::kThreads, 1) bwd_kernel(const __grid_constant__ BwdMaps m, const __grid_constant__ BwdParams p) {
     extern __shared__ unsigned char smem_raw[];
     // a CTA that timed out earlier in this launch (or call) makes the rest return at once
     if (*reinterpret_cast<volatile int*>(p.status) == kDevTimeout) return;
@@ -1039,11 +1084,11 @@ cudaError_t launch_bwd(const AttnBwdArgs& a, cudaStream_t s) {
     int dev = 0;
     if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
     if (dev >= 64 || !(have[parts].load() >> dev & 1)) {
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes<D>);
         if (e != cudaSuccess) return e;
         if (dev < 64) have[parts] |= 1ull << dev;
     }
-    kernel<<<(unsigned)blocks, kThreads, kSmemBytes, s>>>(m, p);
+    kernel<<<(unsigned)blocks, Warps<D>::kThreads, kSmemBytes<D>, s>>>(m, p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     const long long join = (p.kv_parts > 1 && a.dK ? 2 * krows : 0) + (p.q_parts > 1 && a.dQ ? rows : 0);
     if (join) bwd_join_kernel<D><<<(unsigned)((join * (D / 8) + 255) / 256), 256, 0, s>>>(p);
