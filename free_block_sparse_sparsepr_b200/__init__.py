@@ -225,10 +225,13 @@ class SparsePR:
         h = _p()
         _check("sparsepr_create", self.lib.sparsepr_create(ctypes.byref(self.cfg), ctypes.byref(h)))
         self.h = h
-        import torch
-
-        self.device = torch.device("cuda", torch.cuda.current_device())
         self._bwd_bytes = self.attn_bwd_workspace_bytes()
+        try:
+            import torch
+
+            self.device = torch.device("cuda", torch.cuda.current_device())     # the handle's
+        except ImportError:
+            self.device = None
 
     @classmethod
     def from_workload(cls, w, flags=0, **kw):

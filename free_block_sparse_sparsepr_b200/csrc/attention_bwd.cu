@@ -77,8 +77,8 @@ __device__ __forceinline__ void row_terms(const uint4* __restrict__ O, const uin
 // One warp per (KV head z, group): the tiles (start row, valid rows <= 128) of the other side's
 // groups that the route pairs with it, runs of touching groups merged. Warps [0, P Gq) walk their
 // route row; the next P Gk collect the rows that hold their key group (binary search, the kept ids
-// ascend); the last 2 P cut each side's own groups into tiles. Ids and offsets out of range
-// are skipped and reported in the status word, so every tile stays inside [0, N).
+// ascend); the last 2 P cut each side's own groups into tiles. Ids out of range or order and offsets out
+// of range are skipped and reported in the status word, so every tile stays inside [0, N).
 struct ListParams {
     const int32_t *rowptr, *kg, *qoff, *koff;
     int2 *klist, *qlist;
@@ -98,7 +98,7 @@ __device__ void tile_lists(const ListParams& l, int wid, int lane) {
         const int32_t* off = (i & 1) ? koff + (long long)z * (Gk + 1) : qoff + (long long)z * (Gq + 1);
         const int cap = (i & 1) ? l.kv_tiles : l.q_tiles;
         int4* out = ((i & 1) ? l.ktile : l.qtile) + (long long)z * cap;
-        bool bad = false;
+        bool bad = off[0] != 0 || off[G] != N;       // rows that no group holds would get no gradient
         int before = 0;
         for (int g0 = 0; g0 < G; g0 += 32) {
             int n = 0, lo = 0, hi = 0;
@@ -161,7 +161,7 @@ __device__ void tile_lists(const ListParams& l, int wid, int lane) {
             int grp = -1;
             if (rows) {
                 grp = kept[c];
-                if (grp < 0 || grp >= Gk) {
+                if (grp < 0 || grp >= Gk || (c > own_row.x && kept[c - 1] >= grp)) {      // out of range or order
                     bad = true;
                     grp = -1;
                 }
@@ -1022,7 +1022,7 @@ BwdLayout bwd_layout(int P, int g, int N, int d, int Gq, int Gk, const BwdParts&
         l.qtile = take((size_t)P * l.qcap * sizeof(int4));
         l.ktile = take((size_t)P * l.kcap * sizeof(int4));
     }
-    l.bytes = at;
+    l.bytes = at + 240;      // the parts start on 256 bytes, the workspace on 16
     return l;
 }
 
@@ -1030,7 +1030,7 @@ template <int D>
 cudaError_t launch_bwd(const AttnBwdArgs& a, cudaStream_t s) {
     const bool sparse = a.rowptr != nullptr;
     const BwdLayout l = bwd_layout(a.P, a.g, a.N, D, a.Gq, a.Gk, a.parts, sparse);
-    char* ws = static_cast<char*>(a.workspace);
+    char* ws = reinterpret_cast<char*>(align256(reinterpret_cast<uintptr_t>(a.workspace)));
     float *nlse2 = reinterpret_cast<float*>(ws + l.nlse2), *nD = reinterpret_cast<float*>(ws + l.nD);
     const long long rows = (long long)a.P * a.g * a.N, krows = (long long)a.P * a.N;
     BwdParams p;

@@ -282,7 +282,7 @@ sparsepr_status rope(const sparsepr_rope_config* c, const void* src, const int32
     for (int i = 0; i < 3; ++i) {
         if (size_of[i] == 1) continue;
         if (stride_of[i] < 0 || stride_of[i] % per16 != 0) return SPARSEPR_ERR_INVALID_ARG;
-        if (stride_of[i] > (1ll << 40)) return SPARSEPR_ERR_UNSUPPORTED;
+        if (stride_of[i] > (1ll << 40) / size_of[i]) return SPARSEPR_ERR_UNSUPPORTED;      // no sum below overflows
         extent += (size_of[i] - 1) * stride_of[i];
     }
     if (bwd) {

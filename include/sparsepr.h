@@ -378,8 +378,8 @@ sparsepr_status sparsepr_dense_attn_lse(sparsepr_handle h, const void* Q, const 
  * the Q, K, V that sparsepr_permute gathered, in the ORIGINAL token order. A query row without kept
  * keys (lse = -inf) has dQ = 0 and adds nothing; a key that no query group keeps has dK = dV = 0.
  * Only kperm, koff, qperm and qoff of `part` and rowptr and kg of `route` are read. Ids, offsets
- * and permutation entries out of range are skipped and reported as SPARSEPR_ERR_DEVICE in the
- * device status word.
+ * and permutation entries out of range, ids out of order and offsets that leave rows out are
+ * skipped and reported as SPARSEPR_ERR_DEVICE in the device status word.
  *
  * dQ may be NULL, or dK and dV both, to leave those gradients out. No output may overlap an input
  * or another output. workspace: caller-owned device memory, 16-byte aligned, of at least
@@ -387,7 +387,8 @@ sparsepr_status sparsepr_dense_attn_lse(sparsepr_handle h, const void* Q, const 
  * finished; calls with different workspaces may overlap. Nothing else of the handle is written but
  * the device status word, and the calls can be captured into a graph.
  * SPARSEPR_ERR_WORKSPACE: workspace too small. SPARSEPR_ERR_INVALID_ARG also when the handle's
- * device is not the current one.
+ * device is not the current one. While the device status word holds SPARSEPR_ERR_TIMEOUT (until
+ * sparsepr_device_status reads it) the gradients are left unwritten.
  */
 sparsepr_status sparsepr_attn_bwd_workspace(sparsepr_handle h, size_t* bytes);
 sparsepr_status sparsepr_dense_attn_bwd(sparsepr_handle h, const void* Q, const void* K, const void* V,

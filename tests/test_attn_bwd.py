@@ -68,6 +68,8 @@ DENSE = [
     (1, 1, 1, 1, 64), (1, 2, 1, 1, 128), (2, 2, 2, 2, 128), (1, 2, 2, 63, 64), (1, 3, 1, 127, 128), (1, 1, 1, 128, 128),
     (1, 4, 2, 129, 64), (2, 4, 1, 257, 128), (1, 6, 2, 391, 64), (1, 2, 2, 640, 128), (3, 5, 5, 1000, 128),
     (1, 8, 1, 1153, 128), (1, 1, 1, 2600, 64),
+    # more tiles than SMs, streams longer than the rings
+    (4, 16, 8, 1100, 64), (2, 24, 12, 1030, 128),
 ]
 
 
@@ -196,6 +198,13 @@ def test_skipped_gradients_and_own_buffers():
         assert got[0].data_ptr() == wide[1].data_ptr() and torch.equal(got[0], dq)
         assert (wide[0] == 7).all() and (wide[2] == 7).all()
         assert (ws[:256] == 0x5A).all() and (ws[256 + n:] == 0x5A).all()
+        # a workspace that starts on 16 bytes only, on the default stream given by its pointer
+        ws.fill_(0x5A)
+        torch.cuda.synchronize()
+        got = h.dense_attn_bwd(Q, K, V, O, lse, dO, workspace=ws[16:16 + n], stream=0)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, (dq, dk, dv)))
+        assert (ws[:16] == 0x5A).all() and (ws[16 + n:] == 0x5A).all()
 
 
 @gpu
@@ -278,7 +287,8 @@ def test_out_of_range_ids_are_reported():
         torch.cuda.synchronize()
         assert h.device_status() == 0
         for name, at, value in (("kg", (0, 1), G), ("kg", (0, 2), -3), ("qperm", (0, 5), N), ("kperm", (0, 9), -1),
-                                ("rowptr", (0, 2), 10 ** 6), ("koff", (0, 2), N + 5), ("qoff", (0, 1), -7)):
+                                ("rowptr", (0, 2), 10 ** 6), ("koff", (0, 2), N + 5), ("qoff", (0, 1), -7),
+                                ("kg", (0, 1), 0), ("kg", (0, 0), G - 1), ("qoff", (0, 0), 3), ("koff", (0, G), N - 1)):
             bad = {k: v.clone() for k, v in t.items()}
             bad[name][at] = value
             h.blocksparse_attn_bwd(Q, K, V, *_structs(bad), *args)

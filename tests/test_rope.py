@@ -227,6 +227,7 @@ def _config(**kw):
     (dict(dtype=2), 1), (dict(width=(63, 0, 0)), 1), (dict(width=(64, 2, 0), axes=2), 1), (dict(width=(0, 0, 0)), 1),
     (dict(stride_n=100), 1), (dict(stride_h=-64), 1), (dict(pos_stride_b=-1), 1), (dict(amplitude=float("inf")), 1),
     (dict(freq=float("nan")), 1), (dict(B=1 << 20, H=1 << 10, N=1 << 10), 2), (dict(stride_n=1 << 41), 2),
+    (dict(stride_n=1 << 39), 2),
 ])
 def test_c_refusals_without_gpu(kw, code):
     lib = spr.load_library()
