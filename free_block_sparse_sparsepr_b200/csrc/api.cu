@@ -145,6 +145,7 @@ struct sparsepr_handle_s {
     // backward passes: CTAs per tile and workspace bytes, dense [0] and block-sparse [1]
     spr::BwdParts bwd_parts[2] = {};
     size_t bwd_bytes[2] = {};
+    int bwd_attributes = 0;
 };
 
 namespace {
@@ -988,6 +989,7 @@ sparsepr_status attn_bwd_impl(sparsepr_handle h, const void* Q, const void* K, c
     a.dQ = static_cast<bf16*>(dQ); a.dK = static_cast<bf16*>(dK); a.dV = static_cast<bf16*>(dV);
     a.workspace = workspace;
     a.status = h->dev_status;
+    a.attributes = &h->bwd_attributes;
     a.parts = h->bwd_parts[route != nullptr];
     a.P = h->P; a.g = h->g; a.N = c.N; a.d = c.d; a.Gq = c.Gq; a.Gk = c.Gk;
     if (route) {

@@ -199,6 +199,7 @@ struct AttnBwdArgs {
     bf16 *dQ, *dK, *dV;
     void* workspace;
     int* status;
+    int* attributes;                     // host: which kernels' attributes the handle has set (0 at first)
     BwdParts parts;
     int P, g, N, d, Gq, Gk;
 };

@@ -235,6 +235,30 @@ def test_non_finite_rows_stay_apart():
 
 
 @gpu
+@pytest.mark.parametrize("d", [64, 128])
+def test_nan_is_not_lost(d):
+    """A NaN in a query reaches every key's gradients, one in a key every query's, wherever in the tile it stands."""
+    _need_gpu()
+    shape = (1, 1, 1, 200, d)
+    Q, K, V, dO = _inputs(8, *shape)
+    O, lse = forward_reference(Q, K, V)
+    O, lse = O.bfloat16(), lse.float()
+    with _handle(*shape) as h:
+        for i in list(range(20)) + [63, 64, 100, 127, 128, 199]:
+            bad = Q.clone()
+            bad[0, 0, i, 3] = math.nan
+            dq, dk, dv = h.dense_attn_bwd(bad, K, V, O, lse, dO)
+            assert dq[0, 0, i].isnan().all() and dk.isnan().all() and dv.isnan().all(), i
+            rest = torch.arange(200) != i
+            assert torch.isfinite(dq[0, 0, rest.cuda()]).all(), i
+            bad = K.clone()
+            bad[0, 0, i, 3] = math.nan
+            dq, dk, dv = h.dense_attn_bwd(Q, bad, V, O, lse, dO)
+            assert dq.isnan().all() and dk[0, 0, i].isnan().all() and dv[0, 0, i].isnan().all(), i
+            assert torch.isfinite(dk[0, 0, rest.cuda()]).all() and torch.isfinite(dv[0, 0, rest.cuda()]).all(), i
+
+
+@gpu
 def test_other_stream_two_calls_at_once_and_graph():
     _need_gpu()
     B, Hq, Hkv, N, d, G = 1, 4, 2, 700, 128, 8
