@@ -443,46 +443,44 @@ __device__ __forceinline__ void load_cols(uint32_t taddr, uint32_t (&v)[kH][32])
     if (kH == 2) tc::regs_after_wait(v[kH - 1]);
 }
 
-// One fp32 accumulator row of D TMEM columns, times `scale`, rounded to bf16 into `out`.
-template <int D>
-__device__ __forceinline__ void store_acc_row(uint32_t tacc, float scale, bf16* out, bool zero) {
+// A warp's 32 accumulator rows of N TMEM columns, times `scale`, to global rows of T (bf16, or fp32 for
+// partial sums); `row` is the place of this lane's row (null: not stored). The lanes hold a row each, so
+// storing from there would touch 32 rows with every instruction. The rows go through `stage` instead (room
+// for 32 N elements of T, their 16-byte pieces swapped within a row against bank conflicts) and leave as
+// whole rows: 3260 cycles of a tile's 90000 for dV and dK at N = 4096, d = 128, where stores from the
+// lanes took 6350, and 1750 for dQ, where they took 3190; 1-2% of the call.
+template <int N, typename T>
+__device__ __forceinline__ void store_acc_rows(uint32_t tacc, unsigned char* stage, int lane, float scale, bool zero, T* row) {
+    constexpr int kPer = 16 / sizeof(T), kPieces = N / kPer, kRows = 32 / kPieces;      // elements a piece, pieces a row, rows a step
+    uint4* st = reinterpret_cast<uint4*>(stage);
 #pragma unroll
-    for (int c = 0; c < D / 32; ++c) {
+    for (int c = 0; c < N / 32; ++c) {
         uint32_t v[32];
         tc::tmem_ld32(tacc + 32 * c, v);
         tc::tmem_wait_ld();
         tc::regs_after_wait(v);
-        if (!out) continue;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            uint32_t w[4];
+        for (int i = 0; i < 32; ++i) v[i] = zero ? 0u : __float_as_uint(__uint_as_float(v[i]) * scale);
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                w[e] = zero ? 0u
-                            : bf16x2(__uint_as_float(v[8 * q + 2 * e]) * scale, __uint_as_float(v[8 * q + 2 * e + 1]) * scale);
-            *reinterpret_cast<uint4*>(out + 32 * c + 8 * q) = make_uint4(w[0], w[1], w[2], w[3]);
+        for (int q = 0; q < 32 / kPer; ++q) {
+            uint4 u;
+            if (sizeof(T) == 2)
+                u = make_uint4(bf16x2(__uint_as_float(v[8 * q]), __uint_as_float(v[8 * q + 1])),
+                               bf16x2(__uint_as_float(v[8 * q + 2]), __uint_as_float(v[8 * q + 3])),
+                               bf16x2(__uint_as_float(v[8 * q + 4]), __uint_as_float(v[8 * q + 5])),
+                               bf16x2(__uint_as_float(v[8 * q + 6]), __uint_as_float(v[8 * q + 7])));
+            else
+                u = make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+            st[lane * kPieces + ((c * (32 / kPer) + q) ^ (lane & (kPieces - 1)))] = u;
         }
     }
-}
-
-// The same row as it is, into fp32 partial sums.
-template <int D>
-__device__ __forceinline__ void store_part_row(uint32_t tacc, float* out, bool zero) {
+    __syncwarp();
 #pragma unroll
-    for (int c = 0; c < D / 32; ++c) {
-        uint32_t v[32];
-        tc::tmem_ld32(tacc + 32 * c, v);
-        tc::tmem_wait_ld();
-        tc::regs_after_wait(v);
-        if (!out) continue;
-#pragma unroll
-        for (int i = 0; i < 32; i += 8) {
-            if (zero)
-                for (int e = 0; e < 8; ++e) v[i + e] = 0u;
-            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(out + 32 * c + i), "r"(v[i]),
-                         "r"(v[i + 1]), "r"(v[i + 2]), "r"(v[i + 3]), "r"(v[i + 4]), "r"(v[i + 5]), "r"(v[i + 6]), "r"(v[i + 7])
-                         : "memory");
-        }
+    for (int i = 0; i < kPieces; ++i) {
+        const int r = i * kRows + lane / kPieces, piece = lane % kPieces;
+        T* to = reinterpret_cast<T*>(__shfl_sync(kFull, reinterpret_cast<unsigned long long>(row), r));
+        const uint4 u = st[r * kPieces + (piece ^ (r & (kPieces - 1)))];
+        if (to) *reinterpret_cast<uint4*>(to + piece * kPer) = u;
     }
 }
 
@@ -767,12 +765,15 @@ __device__ __forceinline__ void dkv_tile(const BwdMaps& m, const BwdParams& p, u
             constexpr int kN = D / (W::kWgs / 2);
             const int is_dk = w & 1, col = (w >> 1) * kN;
             const uint32_t acc = c.tmem + (is_dk ? kTDK : kTDV) + col + lane_off;
+            // the streamed tiles have all been used: their buffers take the rows
+            unsigned char* stage = c.sbase + kOffBuf + c.warp * (32 * kN * 4);
+            static_assert(4 * W::kWgs * 32 * kN * 4 <= 8 * kRegion, "staging");
             if (PARTS && p.kv_parts > 1) {
                 const long long row = (part * 2 + is_dk) * p.krows + (long long)z * p.N + klo + r;
-                store_part_row<kN>(acc, r < kn ? p.kv_part + row * D + col : nullptr, iters == 0);
+                store_acc_rows<kN, float>(acc, stage, c.lane, 1.f, iters == 0, r < kn ? p.kv_part + row * D + col : nullptr);
             } else {
                 bf16* out = out_row<D>(is_dk ? p.dK : p.dV, p.kperm, z, p.N, klo + r, r < kn, z, p.status);
-                store_acc_row<kN>(acc, is_dk ? p.scale : 1.f, out ? out + col : nullptr, iters == 0);
+                store_acc_rows<kN, bf16>(acc, stage, c.lane, is_dk ? p.scale : 1.f, iters == 0, out ? out + col : nullptr);
             }
         }
     }
@@ -930,12 +931,14 @@ __device__ __forceinline__ void dq_tile(const BwdMaps& m, const BwdParams& p, un
         if (w < 2 && __all_sync(kFull, ok && tc::mbar_wait(c.bar(kDone), 0, c.abort_flag))) {
             tc::fence_after_sync();
             const uint32_t acc = c.tmem + kTDQ + w * kN + lane_off;
+            unsigned char* stage = c.sbase + kOffK + c.warp * (32 * kN * 4);     // as in the other pass
+            static_assert(8 * 32 * kN * 4 <= (kKStages + kVStages) * 2 * kRegion, "staging");
             if (PARTS && p.q_parts > 1) {
                 float* out = p.q_part + (part * p.qrows + (long long)x * p.N + qlo + r) * D + w * kN;
-                store_part_row<kN>(acc, r < qn ? out : nullptr, nt == 0);
+                store_acc_rows<kN, float>(acc, stage, c.lane, 1.f, nt == 0, r < qn ? out : nullptr);
             } else {
                 bf16* out = out_row<D>(p.dQ, p.qperm, x, p.N, qlo + r, r < qn, z, p.status);
-                store_acc_row<kN>(acc, p.scale, out ? out + w * kN : nullptr, nt == 0);
+                store_acc_rows<kN, bf16>(acc, stage, c.lane, p.scale, nt == 0, out ? out + w * kN : nullptr);
             }
         }
     }
