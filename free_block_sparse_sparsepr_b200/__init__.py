@@ -159,13 +159,16 @@ def _stream(stream) -> int | None:
     return stream.cuda_stream
 
 
+_HERE = contextlib.nullcontext()
+
+
 def _on(device, stream):
     """Context with `device` current and, if `stream` is given, that stream current too, so that
     memory taken inside belongs to the stream that uses it."""
     import torch
 
     if stream is None and device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
+        return _HERE
     ctx = contextlib.ExitStack()
     ctx.enter_context(torch.cuda.device(device))
     if stream is not None:
@@ -611,7 +614,8 @@ class Rope:
         B, N, H, d = x.shape
         with _on(x.device, stream):
             if out is None:
-                out = torch.empty((B, H, N, d), dtype=torch.bfloat16, device=x.device)
+                out = (x.new_empty((B, H, N, d)) if x.dtype is torch.bfloat16 else      # half a microsecond less
+                       torch.empty((B, H, N, d), dtype=torch.bfloat16, device=x.device))
             else:
                 _want("out", out, (B, H, N, d), torch.bfloat16, x.device)
             _check("sparsepr_rope", self.lib.sparsepr_rope(cfg, x.data_ptr(), pos.data_ptr(), out.data_ptr(),
@@ -629,7 +633,8 @@ class Rope:
         _want("dy", dy, (B, H, N, d), torch.bfloat16, dy.device)
         with _on(dy.device, stream):
             if out is None:
-                out = torch.empty((B, N, H, d), dtype=dtype or torch.bfloat16, device=dy.device)
+                out = (dy.new_empty((B, N, H, d)) if dtype is None else
+                       torch.empty((B, N, H, d), dtype=dtype, device=dy.device))
             elif tuple(out.shape) != (B, N, H, d) or out.device != dy.device:
                 raise ValueError(f"out: expected [{B}, {N}, {H}, {d}] on {dy.device}, got {tuple(out.shape)} on {out.device}")
             cfg = self._config(out, pos)
