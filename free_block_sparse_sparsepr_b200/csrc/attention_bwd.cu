@@ -39,7 +39,8 @@ struct BwdParams {
     int kv_tiles, q_tiles;                  // most key tiles of a KV head, query tiles of a query head
     int kv_parts, q_parts;                  // CTAs that share a tile's stream
     float *kv_part, *q_part;                // their fp32 sums: [part][dV, dK][P N][D], [part][P g N][D]
-    int kv_blocks;                          // CTAs of dK and dV, before those of dQ
+    int kv_blocks;                          // CTAs of dK and dV
+    int kv_first, q_early;                  // launch order: so many of dK and dV, so many of dQ, then the others of each
     float scale, scale_log2;
 };
 
@@ -946,7 +947,8 @@ __device__ __forceinline__ void dq_tile(const BwdMaps& m, const BwdParams& p, un
 }
 
 // Both passes in one launch: the CTAs of dK and dV come first, being the longer ones, and those of dQ
-// fill the SMs that they leave idle at their end.
+// fill the SMs that they leave idle at their end; where that ends sooner, some of dQ go before the last of
+// dK and dV.
 template <int D>
 constexpr int kSmemBytes = kv::Layout<D>::kSmem > dq::kSmem ? kv::Layout<D>::kSmem : dq::kSmem;
 
@@ -955,12 +957,12 @@ __global__ void __launch_bounds__(Warps<D>::kThreads, 1) bwd_kernel(const __grid
     extern __shared__ unsigned char smem_raw[];
     // a CTA that timed out earlier in this launch (or call) makes the rest return at once
     if (*reinterpret_cast<volatile int*>(p.status) == kDevTimeout) return;
-    const int b = blockIdx.x;
-    if (b < p.kv_blocks) {
-        const int t = PARTS ? b / p.kv_parts : b;
-        dkv_tile<D, PARTS>(m, p, smem_raw, t / p.kv_tiles, t % p.kv_tiles, PARTS ? b % p.kv_parts : 0);
+    const int b = blockIdx.x, early = b - p.kv_first;
+    if (early < 0 || (early >= p.q_early && b < p.kv_blocks + p.q_early)) {
+        const int i = early < 0 ? b : b - p.q_early, t = PARTS ? i / p.kv_parts : i;
+        dkv_tile<D, PARTS>(m, p, smem_raw, t / p.kv_tiles, t % p.kv_tiles, PARTS ? i % p.kv_parts : 0);
     } else {
-        const int i = b - p.kv_blocks, t = PARTS ? i / p.q_parts : i;
+        const int i = early < p.q_early ? early : b - p.kv_blocks, t = PARTS ? i / p.q_parts : i;
         dq_tile<D, PARTS>(m, p, smem_raw, t / p.q_tiles, t % p.q_tiles, PARTS ? i % p.q_parts : 0);
     }
 }
@@ -1085,6 +1087,9 @@ cudaError_t launch_bwd(const AttnBwdArgs& a, cudaStream_t s) {
         return cudaErrorInvalidValue;
     p.kv_blocks = a.dK ? p.kv_tiles * a.P * p.kv_parts : 0;
     const long long blocks = p.kv_blocks + (a.dQ ? (long long)p.q_tiles * a.P * a.g * p.q_parts : 0);
+    const bool both = a.dK && a.dQ;
+    p.kv_first = both ? p.kv_blocks - a.parts.kv_late : p.kv_blocks;
+    p.q_early = both ? a.parts.q_early : 0;
     const bool parts = p.kv_parts > 1 || p.q_parts > 1;
     const auto kernel = parts ? bwd_kernel<D, true> : bwd_kernel<D, false>;
     if (!(*a.attributes & 1 << parts)) {
@@ -1101,15 +1106,39 @@ cudaError_t launch_bwd(const AttnBwdArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-// How many CTAs share a tile's stream: the pair that a model of the launch expects to end first. An
-// SM runs one CTA at a time, those of dK/dV first. Times in microseconds at 1.9 GHz: 1.42 for a dK/dV
-// tile, 1.0 for a dQ tile, 2.5 for a CTA's start and end; the join of the parts' sums takes 2.5 for its
-// launch and 1 per 4 MB written and read back. Few CTAs with long streams gain most, and a number of
+// How many CTAs share a tile's stream, and the order of the launch: what a model of it expects to end
+// first. An SM runs one CTA at a time, in launch order. Times in microseconds at 1.9 GHz, fitted to whole
+// launches: 1.42 for a dK/dV tile, 1.0 for a dQ tile, 2.5 for a CTA's start and end; the join of the parts'
+// sums takes 2.5 for its launch and 1 per 4 MB written and read back. Few CTAs with long streams gain most, and a number of
 // CTAs just past a multiple of the SMs is stepped over. On the device, whole against shared (d = 128, one
 // sample): 4 query heads on 1 KV head, 1000 tokens 54 against 17 us; 3 on 1, 4096 tokens 142 against 85;
 // 12 heads, 1024 tokens 30 against 45 (left whole).
+struct BwdModel {
+    double nk, nq, tk, tq;                  // CTAs of dK and dV, of dQ; their times
+    int sms;
+    // The end of the launch if `m` SMs go on to dQ a turn of dK and dV before the others.
+    double end(double m) const {
+        const double whole = floor(nk / sms), rest = nk - whole * sms;
+        // SMs, and when they turn to dQ
+        const double n[3] = {m, sms - 2 * m - rest, rest + m}, at[3] = {(whole - 1) * tk, whole * tk, (whole + 1) * tk};
+        double t = fmax((nk * tk + nq * tq) / sms, n[2] > 0 ? at[2] : at[1]);
+        for (int i = 0; i < 64; ++i) {
+            double fit = 0, next = 1e30;
+            for (int c = 0; c < 3; ++c) {
+                if (n[c] <= 0) continue;
+                const double ran = floor((t - at[c]) / tq + 1e-6);
+                fit += n[c] * fmax(ran, 0.0);
+                next = fmin(next, at[c] + (ran + 1) * tq);
+            }
+            if (fit >= nq) break;
+            t = next;       // on to the next end of a dQ CTA
+        }
+        return t;
+    }
+};
+
 BwdParts attn_bwd_parts(int P, int g, int N, int d, bool sparse, int sms) {
-    BwdParts best = {1, 1};
+    BwdParts best = {1, 1, 0, 0};
     const double tiles = (N + kTile - 1) / kTile;
     // of a route neither the density nor the groups' sizes are known here: a quarter of the keys, and
     // a quarter more tiles than whole ones
@@ -1120,27 +1149,31 @@ BwdParts attn_bwd_parts(int P, int g, int N, int d, bool sparse, int sms) {
     for (int kv : kChoices)
         for (int q : kChoices) {
             if ((kv > 1 && kv > len * g) || (q > 1 && q > len)) continue;
-            const double nk = ctas * P * kv, nq = ctas * P * g * q, tk = 1.42 * ceil(len * g / kv) + 2.5, tq = ceil(len / q) + 2.5;
-            const double whole = floor(nk / sms), rest = nk - whole * sms;     // `rest` SMs run one dK/dV CTA more
-            // the dQ CTAs start at whole tk on the other SMs and at (whole + 1) tk on those
-            double t = (nk * tk + nq * tq) / sms;
-            t = fmax(t, (rest > 0 ? whole + 1 : whole) * tk);
-            auto fit = [&](double end) {
-                const double late = floor((end - (whole + 1) * tk) / tq + 1e-6), early = floor((end - whole * tk) / tq + 1e-6);
-                return rest * fmax(late, 0.0) + (sms - rest) * fmax(early, 0.0);
-            };
-            for (int i = 0; i < 32 && fit(t) < nq; ++i) {      // on to the next end of a dQ CTA
-                const double e0 = (floor((t - whole * tk) / tq + 1e-6) + 1) * tq + whole * tk;
-                const double e1 = rest > 0 ? (floor((t - (whole + 1) * tk) / tq + 1e-6) + 1) * tq + (whole + 1) * tk : e0;
-                t = fmin(e0, e1);
-            }
+            const BwdModel w = {ctas * P * kv, ctas * P * g * q, 1.42 * ceil(len * g / kv) + 2.5, ceil(len / q) + 2.5, sms};
+            double t = w.end(0);
             const double mb = 4e-6 * d * N * (double)P * ((kv > 1 ? 2.0 * kv : 0) + (q > 1 ? (double)g * q : 0));
             if (kv > 1 || q > 1) t += 2.5 + 2 * mb / 4;
             if (t < best_t * 0.97) {      // a gain below the model's error is none
                 best_t = t;
-                best = {kv, q};
+                best = {kv, q, 0, 0};
             }
         }
+    // The order, for equal streams: m SMs turn to dQ before their last CTA of dK and dV, m others run one
+    // more of those (12 heads, 4096 tokens: 277 -> 271 us with m = 28; 16 on 4 heads, 2 x 2311: 257 -> 252 with
+    // 32). Here the times are those of steady tiles and of whole CTAs, by clock reads in long launches.
+    if (!sparse && best.kv == 1 && best.q == 1) {
+        const BwdModel w = {ctas * P, ctas * P * g, 1.35 * len * g + 4.4, 0.98 * len + 3.1, sms};
+        const int rest = (int)w.nk % sms, each = (int)ceil(w.tk / w.tq);
+        best_t = w.end(0);
+        for (int m = 1; w.nk >= sms && rest + 2 * m <= sms && (double)m * each <= w.nq; ++m) {
+            const double t = w.end(m);
+            if (t < best_t * 0.995) {
+                best_t = t;
+                best.kv_late = rest + m;
+                best.q_early = m * each;
+            }
+        }
+    }
     return best;
 }
 

@@ -190,6 +190,7 @@ cudaError_t launch_attn_probe(const bf16* Q, const bf16* K, const bf16* V, const
 // skips it, dK and dV null skips both. workspace: attn_bwd_workspace bytes, 256-byte aligned parts.
 struct BwdParts {
     int kv, q;                           // CTAs that share the stream of a dK/dV tile, of a dQ tile
+    int kv_late, q_early;                // CTAs of dK/dV that are launched after so many of dQ
 };
 BwdParts attn_bwd_parts(int P, int g, int N, int d, bool sparse, int sms);
 struct AttnBwdArgs {

@@ -178,6 +178,25 @@ def test_directional_differences():
 
 
 @gpu
+@pytest.mark.parametrize("shape", [(4, 76, 38, 100, 64), (4, 40, 40, 100, 128), (2, 40, 40, 200, 128)], ids=str)
+def test_one_pass_alone_gives_the_same(shape):
+    """A little over one CTA of dK and dV an SM: some of dQ are launched before the last of those."""
+    _need_gpu()
+    B, Hq, Hkv, N, d = shape
+    Q, K, V, dO = _inputs(N + Hq, *shape)
+    with _handle(*shape) as h:
+        lse = torch.empty((B, Hq, N), device="cuda")
+        O = h.dense_attn(Q, K, V, lse=lse)
+        got = h.dense_attn_bwd(Q, K, V, O, lse, dO)
+        dq = h.dense_attn_bwd(Q, K, V, O, lse, dO, need_dkv=False)[0]
+        _, dk, dv = h.dense_attn_bwd(Q, K, V, O, lse, dO, need_dq=False)
+        torch.cuda.synchronize()
+        assert h.device_status() == 0
+    assert all(torch.equal(a, b) for a, b in zip(got, (dq, dk, dv)))
+    check_gradients(got, backward_reference(Q, K, V, O, lse, dO), f"dense {shape}")
+
+
+@gpu
 def test_skipped_gradients_and_own_buffers():
     _need_gpu()
     shape = (1, 4, 2, 200, 128)
