@@ -527,7 +527,7 @@ sparsepr_status sparsepr_create(const sparsepr_config* cfg, sparsepr_handle* out
     h->Gmax = c.Gk > c.Gq ? c.Gk : c.Gq;
     h->timing = (c.flags & SPARSEPR_FLAG_STAGE_TIMING) != 0;
     for (int i = 0; i < 2; ++i) {
-        h->bwd_parts[i] = spr::attn_bwd_parts(h->P, h->g, c.N, c.d, i == 1, h->num_sms);
+        h->bwd_parts[i] = spr::attn_bwd_parts(h->P, h->g, c.N, c.d, c.Gq, c.Gk, i == 1, h->num_sms);
         h->bwd_bytes[i] = spr::attn_bwd_workspace(h->P, h->g, c.N, c.d, c.Gq, c.Gk, h->bwd_parts[i], i == 1);
     }
     const size_t P = h->P, Hp = h->Hp, N = c.N, d = c.d, M = h->M > 0 ? h->M : 1, r = c.r > 0 ? c.r : 1;

@@ -29,13 +29,13 @@ struct BwdParams {
     const float *nlse2, *nD;                // per query row: -lse log2(e), -dO.O
     bf16 *dQ, *dK, *dV;
     const int32_t *qperm, *kperm;           // output row of each position (null: the position itself)
-    const int2 *klist, *qlist;              // kept key tiles of each query group, query tiles of each key group
+    const int2 *klist, *qlist;              // kept key tiles of each query group (or two), query tiles of each key group
     const int32_t *kcnt, *qcnt;             // their numbers
-    const int4 *qtile, *ktile;              // [P][q_tiles], [P][kv_tiles]: group, first row and rows of each tile (0: none)
+    const int4 *qtile, *ktile;              // [P][q_tiles], [P][kv_tiles]: list, first row, rows of each tile (0: none), split
     int kcap, qcap;                         // list entries per group
     int* status;
     long long krows, qrows;                 // P N, P g N
-    int N, g, Gq, Gk;
+    int N, g, Gq, Gk;                       // Gq, Gk: lists per KV head
     int kv_tiles, q_tiles;                  // most key tiles of a KV head, query tiles of a query head
     int kv_parts, q_parts;                  // CTAs that share a tile's stream
     float *kv_part, *q_part;                // their fp32 sums: [part][dV, dK][P N][D], [part][P g N][D]
@@ -81,25 +81,73 @@ __device__ __forceinline__ void row_terms(const uint4* __restrict__ O, const uin
 // One warp per (KV head z, group): the tiles (start row, valid rows <= 128) of the other side's
 // groups that the route pairs with it, runs of touching groups merged. Warps [0, P Gq) walk their
 // route row; the next P Gk collect the rows that hold their key group (binary search, the kept ids
-// ascend); the last 2 P cut each side's own groups into tiles. Ids out of range or order and offsets out
-// of range are skipped and reported in the status word, so every tile stays inside [0, N).
+// ascend); without `joined` the last 2 P cut each side's own groups into tiles. Ids out of range or order and
+// offsets out of range are skipped and reported in the status word, so every tile stays inside [0, N).
+//
+// Joined: a tile may hold the last rows of one group and the first of the next that is not empty, so that
+// groups of 100 or 130 rows do not leave half of the lanes idle. Its list is the union of both groups' lists,
+// each entry with the groups that keep it (1 the first, 2 the second, 3 both; two more warps per group), and
+// the sums skip the other group's lanes. Which tiles to join depends on how much the lists share: the cut is
+// chosen per KV head and side with the lists at hand (joined_tiles). 24 heads x 8192 tokens, 64 uneven groups,
+// 22% kept: the owned tiles are filled to 1.0 in place of 0.67.
+constexpr int kMaxGroups = 1024;            // of a side
 struct ListParams {
     const int32_t *rowptr, *kg, *qoff, *koff;
     int2 *klist, *qlist;
     int32_t *kcnt, *qcnt;
     int4 *qtile, *ktile;
     int* status;
-    int kcap, qcap, q_tiles, kv_tiles, P, N, Gq, Gk;
+    int kcap, qcap, q_tiles, kv_tiles, P, N, Gq, Gk, g, joined;
 };
 
+// Cuts the runs of a list into tiles as they are found.
+struct Runs {
+    int2* out;
+    int cap, lane, nt = 0, lo = 0, hi = 0, cls = 0;
+    bool bad = false;
+    __device__ __forceinline__ void emit() {
+        const int n = (hi - lo + kTile - 1) / kTile;
+        if (nt + n > cap) {     // more tiles than disjoint groups can have
+            bad = true;
+            return;
+        }
+        for (int t = lane; t < n; t += 32) out[nt + t] = make_int2(lo + t * kTile, min(kTile, hi - lo - t * kTile) | cls << 8);
+        nt += n;
+    }
+    // the rows [l, h) that each lane holds (none: h <= l), in lane order, of class c
+    __device__ __forceinline__ void add(int l, int h, int c) {
+        unsigned todo = __ballot_sync(kFull, h > l);
+        while (todo) {
+            const int i = __ffs(todo) - 1;
+            todo &= todo - 1;
+            const int nl = __shfl_sync(kFull, l, i), nh = __shfl_sync(kFull, h, i), nc = __shfl_sync(kFull, c, i);
+            if (nl != hi || nc != cls) {
+                emit();
+                lo = nl;
+                cls = nc;
+            }
+            hi = nh;
+        }
+    }
+};
+
+// Whether the kept ids kept[r.x .. r.y) hold `id`.
+__device__ __forceinline__ bool holds(const int32_t* kept, int2 r, int id) {
+    int b = r.x, e = r.y;
+    while (b < e) {
+        const int m = (b + e) >> 1;
+        if (kept[m] < id) b = m + 1; else e = m;
+    }
+    return b < r.y && kept[b] == id;
+}
+
 __device__ void tile_lists(const ListParams& l, int wid, int lane) {
-    const int32_t *rowptr = l.rowptr, *kg = l.kg, *qoff = l.qoff, *koff = l.koff;
-    const int P = l.P, N = l.N, Gq = l.Gq, Gk = l.Gk;
+    const int P = l.P, N = l.N, Gq = l.Gq, Gk = l.Gk, lists = P * (Gq + Gk);
     int* status = l.status;
-    if (wid >= P * (Gq + Gk)) {
-        const int i = wid - P * (Gq + Gk), z = i >> 1, G = (i & 1) ? Gk : Gq;
+    if (!l.joined && wid >= lists) {
+        const int i = wid - lists, z = i >> 1, G = (i & 1) ? Gk : Gq;
         if (z >= P) return;
-        const int32_t* off = (i & 1) ? koff + (long long)z * (Gk + 1) : qoff + (long long)z * (Gq + 1);
+        const int32_t* off = (i & 1) ? l.koff + (long long)z * (Gk + 1) : l.qoff + (long long)z * (Gq + 1);
         const int cap = (i & 1) ? l.kv_tiles : l.q_tiles;
         int4* out = ((i & 1) ? l.ktile : l.qtile) + (long long)z * cap;
         bool bad = off[0] != 0 || off[G] != N;       // rows that no group holds would get no gradient
@@ -128,14 +176,23 @@ __device__ void tile_lists(const ListParams& l, int wid, int lane) {
         if (__any_sync(kFull, bad) && lane == 0) set_status(status, kDevBounds);
         return;
     }
+    if (wid >= lists * (l.joined ? 2 : 1)) return;
+    const bool pair = wid >= lists;
+    wid -= pair ? lists : 0;
     const bool rows = wid < P * Gq;
-    const int z = rows ? wid / Gq : (wid - P * Gq) / Gk;
+    const int z = rows ? wid / Gq : (wid - P * Gq) / Gk, G = rows ? Gq : Gk, others = rows ? Gk : Gq;
     const int own = rows ? wid % Gq : (wid - P * Gq) % Gk;
-    const int32_t* rp = rowptr + (long long)z * (Gq + 1);
-    const int32_t* kept = kg + (long long)z * Gq * Gk;
-    const int32_t* off = rows ? koff + (long long)z * (Gk + 1) : qoff + (long long)z * (Gq + 1);
-    const int cap = rows ? l.kcap : l.qcap;
-    int2* out = (rows ? l.klist + ((long long)z * Gq + own) * cap : l.qlist + ((long long)z * Gk + own) * cap);
+    const int32_t* rp = l.rowptr + (long long)z * (Gq + 1);
+    const int32_t* kept = l.kg + (long long)z * Gq * Gk;
+    const int32_t *koff = l.koff + (long long)z * (Gk + 1), *qoff = l.qoff + (long long)z * (Gq + 1);
+    const int32_t *off = rows ? koff : qoff, *own_off = rows ? qoff : koff;
+    const int lists_z = G * (l.joined ? 2 : 1);
+    const long long id = (long long)z * lists_z + (pair ? G : 0) + own;
+    int32_t* count = (rows ? l.kcnt : l.qcnt) + id;
+    Runs runs;
+    runs.cap = rows ? l.kcap : l.qcap;
+    runs.out = (rows ? l.klist : l.qlist) + id * runs.cap;
+    runs.lane = lane;
     bool bad = false;
     // the bounds of route row a, empty if they are no range of the kept list
     auto row_range = [&](int a) {
@@ -146,73 +203,154 @@ __device__ void tile_lists(const ListParams& l, int wid, int lane) {
         }
         return r;
     };
-    int nt = 0, cur_lo = 0, cur_hi = 0;
-    auto emit = [&]() {
-        const int n = (cur_hi - cur_lo + kTile - 1) / kTile;
-        if (nt + n > cap) {     // more tiles than disjoint groups can have
+    // the rows of the other side's group k
+    auto bounds = [&](int k) {
+        int2 r = make_int2(off[k], off[k + 1]);
+        if (r.x < 0 || r.y < r.x || r.y > N) {
             bad = true;
-            return;
+            r = make_int2(0, 0);
         }
-        for (int t = lane; t < n; t += 32)
-            out[nt + t] = make_int2(cur_lo + t * kTile, min(kTile, cur_hi - cur_lo - t * kTile));
-        nt += n;
+        return r;
     };
-    const int2 own_row = rows ? row_range(own) : make_int2(0, Gq);
-    for (int c0 = own_row.x; c0 < own_row.y; c0 += 32) {
-        const int c = c0 + lane;
-        int lo = 0, hi = 0;
-        if (c < own_row.y) {
-            int grp = -1;
-            if (rows) {
-                grp = kept[c];
-                if (grp < 0 || grp >= Gk || (c > own_row.x && kept[c - 1] >= grp)) {      // out of range or order
-                    bad = true;
-                    grp = -1;
-                }
-            } else {
-                const int2 r = row_range(c);
-                int b = r.x, e = r.y;
-                while (b < e) {
-                    const int m = (b + e) >> 1;
-                    if (kept[m] < own) b = m + 1; else e = m;
-                }
-                if (b < r.y && kept[b] == own) grp = c;
-            }
-            if (grp >= 0) {
-                lo = off[grp];
-                hi = off[grp + 1];
-                if (lo < 0 || hi < lo || hi > N) {
-                    bad = true;
-                    lo = hi = 0;
-                }
-            }
+    if (pair) {
+        int next = G;       // the next group that is not empty
+        for (int g0 = own + 1; g0 < G && next == G; g0 += 32) {
+            const unsigned some = __ballot_sync(kFull, g0 + lane < G && own_off[min(g0 + lane, G - 1) + 1] > own_off[min(g0 + lane, G - 1)]);
+            if (some) next = g0 + __ffs(some) - 1;
         }
-        unsigned todo = __ballot_sync(kFull, hi > lo);
-        while (todo) {
-            const int i = __ffs(todo) - 1;
-            todo &= todo - 1;
-            const int l = __shfl_sync(kFull, lo, i), h = __shfl_sync(kFull, hi, i);
-            if (l != cur_hi) {
-                emit();
-                cur_lo = l;
+        if (next < G && own_off[own + 1] > own_off[own]) {
+            const int2 r0 = rows ? row_range(own) : make_int2(0, 0), r1 = rows ? row_range(next) : make_int2(0, 0);
+            for (int k0 = 0; k0 < others; k0 += 32) {
+                const int k = k0 + lane;
+                int2 b = make_int2(0, 0);
+                int cls = 0;
+                if (k < others) {
+                    const int2 r = rows ? r0 : row_range(k);
+                    cls = holds(kept, r, rows ? k : own) | holds(kept, rows ? r1 : r, rows ? k : next) << 1;
+                    if (cls) b = bounds(k);
+                }
+                runs.add(b.x, b.y, cls);
             }
-            cur_hi = h;
+            runs.emit();
         }
+    } else {
+        const int2 own_row = rows ? row_range(own) : make_int2(0, Gq);
+        for (int c0 = own_row.x; c0 < own_row.y; c0 += 32) {
+            const int c = c0 + lane;
+            int2 b = make_int2(0, 0);
+            if (c < own_row.y) {
+                int grp = -1;
+                if (rows) {
+                    grp = kept[c];
+                    if (grp < 0 || grp >= Gk || (c > own_row.x && kept[c - 1] >= grp)) {      // out of range or order
+                        bad = true;
+                        grp = -1;
+                    }
+                } else if (holds(kept, row_range(c), own)) {
+                    grp = c;
+                }
+                if (grp >= 0) b = bounds(grp);
+            }
+            runs.add(b.x, b.y, 0);
+        }
+        runs.emit();
     }
-    emit();
-    if (lane == 0) (rows ? l.kcnt + (long long)z * Gq : l.qcnt + (long long)z * Gk)[own] = nt;
-    if (__any_sync(kFull, bad) && lane == 0) set_status(status, kDevBounds);
+    if (lane == 0) *count = runs.nt;
+    if (__any_sync(kFull, bad || runs.bad) && lane == 0) set_status(status, kDevBounds);
 }
 
-// The lists (blocks before `list_blocks`) and the rows' terms (the others) in one launch.
+// The cut of one side of one KV head (z = i / 2; keys where i is odd) into tiles of one or two groups, by one
+// warp. Four ways to deal with a group's last rows, r < 128 of them: a tile of their own; joined with the next
+// group's own last rows where both fit a tile (a tile fewer, and the list no longer than both), those moved to
+// its front; the same filled up; filled up with the next group's first rows always. The lanes 0 to 3 walk one
+// each and count streamed tiles, 3.5 more for a CTA's start and end; the cheapest is written.
+__device__ void joined_tiles(const ListParams& l, int i, int lane) {
+    __shared__ int s_lo[kMaxGroups], s_n[kMaxGroups], s_one[kMaxGroups], s_two[kMaxGroups];
+    __shared__ unsigned short s_id[kMaxGroups];
+    const int z = i >> 1, keys = i & 1, G = keys ? l.Gk : l.Gq, N = l.N;
+    const int32_t* off = keys ? l.koff + (long long)z * (G + 1) : l.qoff + (long long)z * (G + 1);
+    const int32_t* cnt = (keys ? l.qcnt : l.kcnt) + (long long)z * 2 * G;
+    const int cap = keys ? l.kv_tiles : l.q_tiles;
+    int4* out = (keys ? l.ktile : l.qtile) + (long long)z * cap;
+    bool bad = off[0] != 0 || off[G] != N;       // rows that no group holds would get no gradient
+    int m = 0;                                   // groups that are not empty
+    for (int g0 = 0; g0 < G; g0 += 32) {
+        const int grp = g0 + lane;
+        int lo = 0, hi = 0;
+        if (grp < G) {
+            lo = off[grp];
+            hi = off[grp + 1];
+            if (lo < 0 || hi < lo || hi > N) {
+                bad = true;
+                lo = hi = 0;
+            }
+        }
+        const unsigned some = __ballot_sync(kFull, hi > lo);
+        if (hi > lo) {
+            const int at = m + __popc(some & ((1u << lane) - 1));
+            s_lo[at] = lo;
+            s_n[at] = hi - lo;
+            s_one[at] = cnt[grp];
+            s_two[at] = cnt[G + grp];
+            s_id[at] = (unsigned short)grp;
+        }
+        m += __popc(some);
+    }
+    __syncwarp();
+    // calls tile(list, first row, rows, split, streamed tiles)
+    auto walk = [&](int mode, auto tile) {
+        for (int j = 0, o = 0; j < m;) {         // o rows of group j are in tiles
+            const int n = s_n[j], rest = n - o, lo = s_lo[j] + o;
+            int take = 0;
+            if (rest < kTile && mode > 0 && j + 1 < m && s_lo[j + 1] == s_lo[j] + n) {
+                const int next = s_n[j + 1], room = kTile - rest, last = (next - 1) % kTile + 1;
+                take = mode == 3 ? min(room, next) : last > room ? 0 : mode == 2 ? min(room, next) : last;
+            }
+            if (take > 0) tile(G + s_id[j], lo, rest + take, rest, s_two[j]);
+            else tile(s_id[j], lo, min(rest, kTile), 0, s_one[j]);
+            if (rest > kTile) {
+                o += kTile;
+            } else {
+                ++j;
+                o = take;
+                if (take > 0 && take == s_n[j]) {
+                    ++j;
+                    o = 0;
+                }
+            }
+        }
+    };
+    const int heads = keys ? l.g : 1;
+    unsigned long long cost = 0;
+    if (lane < 4) walk(lane, [&](int, int, int, int, int streamed) { cost += 2ull * streamed * heads + 7; });
+    int mode = 0;
+    for (int k = 1; k < 4; ++k)
+        if (__shfl_sync(kFull, cost, k) < __shfl_sync(kFull, cost, mode)) mode = k;
+    int nt = 0;
+    walk(mode, [&](int list, int lo, int rows, int split, int) {
+        if (nt < cap && lane == 0) out[nt] = make_int4(list, lo, rows, split);
+        ++nt;
+    });
+    if (nt > cap) bad = true;                    // more tiles than disjoint groups can have
+    for (int t = nt + lane; t < cap; t += 32) out[t] = make_int4(0, 0, 0, 0);
+    if (__any_sync(kFull, bad) && lane == 0) set_status(l.status, kDevBounds);
+}
+
+// The lists (blocks before `list_blocks`) and the rows' terms (the others) in one launch; the joined tiles
+// read the lists, so then these have a launch of their own and the tiles (a warp a block) take their place.
 template <int D>
 __global__ void __launch_bounds__(256) bwd_prepare_kernel(const ListParams l, int list_blocks, const uint4* O, const uint4* dO,
                                                           const float* lse, float* nlse2, float* nD, long long rows) {
     if ((int)blockIdx.x < list_blocks) {
-        tile_lists(l, (blockIdx.x * blockDim.x + threadIdx.x) >> 5, threadIdx.x & 31);
+        if (!l.joined) tile_lists(l, (blockIdx.x * blockDim.x + threadIdx.x) >> 5, threadIdx.x & 31);
+        else if (threadIdx.x < 32) joined_tiles(l, blockIdx.x, threadIdx.x);
         return;
     }
     row_terms<D>(O, dO, lse, nlse2, nD, rows, (long long)(blockIdx.x - list_blocks) * blockDim.x + threadIdx.x);
+}
+
+__global__ void __launch_bounds__(256) bwd_lists_kernel(const ListParams l) {
+    tile_lists(l, (blockIdx.x * blockDim.x + threadIdx.x) >> 5, threadIdx.x & 31);
 }
 
 // ---------------------------------------------------------------- gradients
@@ -299,15 +437,36 @@ __device__ __forceinline__ void mma_rows(uint32_t d_tmem, uint32_t a, uint32_t b
     }
 }
 
-// D[tmem] (+)= A B over the 128 rows of tile b (MN-major); A is bf16 pairs in 64 TMEM columns.
-template <int D>
-__device__ __forceinline__ void mma_sums(uint32_t d_tmem, uint32_t a_tmem, uint32_t b, bool accumulate, uint32_t go) {
+// Lanes of a tile of two groups, split after `split` rows, that a streamed tile of class `cls` leaves alone.
+struct Lanes {
+    uint32_t first[4];                      // the first group's
+    __device__ __forceinline__ explicit Lanes(int split) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int n = min(max(split - 32 * i, 0), 32);
+            first[i] = n == 32 ? kFull : (1u << n) - 1;
+        }
+    }
+    __device__ __forceinline__ void off(int cls, uint32_t (&o)[4]) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = cls == 1 ? ~first[i] : cls == 2 ? first[i] : 0u;
+    }
+};
+
+// D[tmem] (+)= A B over the 128 rows of tile b (MN-major); A is bf16 pairs in 64 TMEM columns. The lanes of
+// `off` (JOINED) stay as they are, whatever their rows of A hold.
+template <int D, bool JOINED>
+__device__ __forceinline__ void mma_sums(uint32_t d_tmem, uint32_t a_tmem, uint32_t b, const uint32_t (&off)[4], bool accumulate,
+                                         uint32_t go) {
     constexpr uint32_t id = tc::idesc_bf16_f32(kTile, D, 1);
     const uint64_t db = tc::smem_desc_sw128(b, kRegion, 1024);
 #pragma unroll
-    for (int k = 0; k < kTile / 16; ++k)
-        tc::mma_f16_ts_go(d_tmem, a_tmem + (uint32_t)(8 * k), db + (uint64_t)(k * 2048 >> 4), id,
-                          (accumulate || k > 0) ? 1u : 0u, go);
+    for (int k = 0; k < kTile / 16; ++k) {
+        const uint32_t at = a_tmem + (uint32_t)(8 * k);
+        const uint64_t bk = db + (uint64_t)(k * 2048 >> 4);
+        if (JOINED) tc::mma_f16_ts_off_go(d_tmem, at, bk, id, off, 1u, go);
+        else tc::mma_f16_ts_go(d_tmem, at, bk, id, (accumulate || k > 0) ? 1u : 0u, go);
+    }
 }
 
 // D[tmem] += A B^T over one K step of 16: [128][16] tiles without swizzle, as two halves of 8 columns.
@@ -485,6 +644,15 @@ __device__ __forceinline__ void store_acc_rows(uint32_t tacc, unsigned char* sta
     }
 }
 
+// Zeros in N TMEM columns of the warp's lanes.
+template <int N>
+__device__ __forceinline__ void zero_cols(uint32_t taddr) {
+    const uint32_t z[32] = {};
+#pragma unroll
+    for (int c = 0; c < N; c += 32) tc::tmem_st32(taddr + c, z);
+    tc::tmem_wait_st();
+}
+
 // Output row of position `pos` (null: out of range, reported, or not wanted).
 template <int D>
 __device__ __forceinline__ bf16* out_row(bf16* base, const int32_t* perm, long long head, int N, int pos, bool want,
@@ -498,13 +666,15 @@ __device__ __forceinline__ bf16* out_row(bf16* base, const int32_t* perm, long l
     return base + (head * N + row) * D;
 }
 
-// Tile `pair` of one side: rows [lo, lo + n) of group `grp`; false past the last tile. (A table: a
+// Tile `pair` of one side: rows [lo, lo + n) that stream list `grp`, the first `split` of them of a group of
+// their own; false past the last tile. (A table: a
 // search of the group offsets costs a CTA some eight reads of memory one after another.)
-__device__ __forceinline__ bool find_tile(const int4* table, int z, int tiles, int N, int pair, int& grp, int& lo, int& n) {
+__device__ __forceinline__ bool find_tile(const int4* table, int z, int tiles, int N, int pair, int& grp, int& lo, int& n, int& split) {
     const int4 e = table ? __ldg(table + (long long)z * tiles + pair) : make_int4(0, pair * kTile, min(kTile, N - pair * kTile), 0);
     grp = e.x;
     lo = e.y;
     n = e.z;
+    split = e.w;
     return n > 0;
 }
 
@@ -549,7 +719,7 @@ struct Layout {
 };
 }  // namespace kv
 
-template <int D, bool PARTS>
+template <int D, bool PARTS, bool JOINED>
 __device__ __forceinline__ void dkv_tile(const BwdMaps& m, const BwdParams& p, unsigned char* smem_raw, int z, int pair, int part) {
     using namespace kv;
     using W = Warps<D>;
@@ -558,8 +728,8 @@ __device__ __forceinline__ void dkv_tile(const BwdMaps& m, const BwdParams& p, u
     constexpr int kOffExt = L::kOffExt, kOffOne = L::kOffOne, kOffBar = L::kOffBar;
     constexpr int kOf = L::kOf, kQe = L::kQe, kOe = L::kOe, kS = L::kS, kDP = L::kDP, kDone = L::kDone, kLand = L::kLand, kSread = L::kSread,
                   kDPread = L::kDPread, kP = L::kP, kDS = L::kDS, kBars = L::kBars;
-    int grp, klo, kn;
-    if (!find_tile(p.ktile, z, p.kv_tiles, p.N, pair, grp, klo, kn)) return;
+    int grp, klo, kn, split;
+    if (!find_tile(p.ktile, z, p.kv_tiles, p.N, pair, grp, klo, kn, split)) return;
     const int2* list = p.qlist + ((long long)z * p.Gk + grp) * p.qcap;
     const int nt = p.qcnt ? p.qcnt[(long long)z * p.Gk + grp] : (p.N + kTile - 1) / kTile;
     // this CTA's share of the (query head, query tile) stream
@@ -599,17 +769,17 @@ __device__ __forceinline__ void dkv_tile(const BwdMaps& m, const BwdParams& p, u
         auto fetch = [&](int2 e, int head) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int r = 32 * j + c.lane;
+                const int r = 32 * j + c.lane, valid = JOINED ? e.y & 255 : e.y;
                 const long long at = (long long)head * p.N + e.x + r;
-                nl[j] = r < e.y ? __ldg(p.nlse2 + at) : -INFINITY;
-                nd[j] = r < e.y ? __ldg(p.nD + at) : 0.f;
+                nl[j] = r < valid ? __ldg(p.nlse2 + at) : -INFINITY;
+                nd[j] = r < valid ? __ldg(p.nD + at) : 0.f;
             }
         };
         const float inv = 1.f / p.scale_log2;
         int2 e = iters > 0 ? tile(t) : make_int2(0, 0);
         if (iters > 0) fetch(e, x);
         for (int it = 0; it < iters; ++it) {
-            const int s = it % kStages, row = x * p.N + e.x, valid = e.y;
+            const int s = it % kStages, row = x * p.N + e.x, valid = JOINED ? e.y & 255 : e.y;
             if (++t == nt) {
                 t = 0;
                 ++x;
@@ -660,9 +830,14 @@ __device__ __forceinline__ void dkv_tile(const BwdMaps& m, const BwdParams& p, u
             mma_ext(tS, c.base + kOffOne, ext(it), go);
             tc::commit_go(c.bar(kS), go);
         };
-        auto issue_dK = [&](int it) {
+        // joined: the lanes that the last tile's and this tile's sums leave alone
+        const Lanes lanes(split);
+        uint32_t off_last[4] = {}, off[4] = {};
+        int t = 0, cls = 0;
+        if (JOINED && iters > 0) cls = tile(t).y >> 8;
+        auto issue_dK = [&](int it, const uint32_t (&skip)[4]) {
             if (!wait(kDS, it)) return false;
-            mma_sums<D>(c.tmem + kTDK, c.tmem + kTDS, q(it), it > 0, go);
+            mma_sums<D, JOINED>(c.tmem + kTDK, c.tmem + kTDS, q(it), skip, it > 0, go);
             tc::commit_go(c.bar(kQe + it % kStages), go);
             return true;
         };
@@ -675,6 +850,11 @@ __device__ __forceinline__ void dkv_tile(const BwdMaps& m, const BwdParams& p, u
         };
         for (int it = 0; ok && it < iters; ++it) {
             const bool more = it + 1 < iters;
+            if (JOINED) {
+                lanes.off(cls, off);
+                if (++t == nt) t = 0;
+                if (more) cls = tile(t).y >> 8;
+            }
             if (!wait(kOf + it % kStages, it / kStages)) break;
             if (D == 64) {
                 if (it > 0 && !wait(kDPread, it - 1)) break;
@@ -683,20 +863,22 @@ __device__ __forceinline__ void dkv_tile(const BwdMaps& m, const BwdParams& p, u
                     if (!wait(kQf + (it + 1) % kStages, (it + 1) / kStages) || !wait(kSread, it)) break;
                     issue_S(it + 1);
                 }
-                if (it > 0 && !issue_dK(it - 1)) break;
+                if (it > 0 && !issue_dK(it - 1, off_last)) break;
             } else {
                 if (!wait(kSread, it)) break;
                 issue_dP(it);
-                if (it > 0 && !issue_dK(it - 1)) break;
+                if (it > 0 && !issue_dK(it - 1, off_last)) break;
                 if (more) {
                     if (!wait(kQf + (it + 1) % kStages, (it + 1) / kStages) || !wait(kDPread, it)) break;
                     issue_S(it + 1);
                 }
             }
             if (!wait(kP, it)) break;
-            mma_sums<D>(c.tmem + kTDV, c.tmem + kTP, o(it), it > 0, go);
+            mma_sums<D, JOINED>(c.tmem + kTDV, c.tmem + kTP, o(it), off, it > 0, go);
             tc::commit_go(c.bar(kOe + it % kStages), go);
-            if (!more) issue_dK(it);
+            if (!more) issue_dK(it, off);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) off_last[i] = off[i];
         }
         // every issued MMA completes before the sums are read and TMEM is released
         tc::commit_go(c.bar(kDone), go);
@@ -708,6 +890,9 @@ __device__ __forceinline__ void dkv_tile(const BwdMaps& m, const BwdParams& p, u
         const uint32_t tS = c.tmem + kTS + W::kCols * w + lane_off, tDP = c.tmem + L::kTDP + W::kCols * w + lane_off;
         const uint32_t tP = c.tmem + kTP + W::kCols / 2 * w + lane_off, tDS = c.tmem + kTDS + W::kCols / 2 * w + lane_off;
         const uint64_t cc = pk2(p.scale_log2, p.scale_log2);
+        // the first sums into a lane need not be the tile's first: all start from zero, before this thread says
+        // that it has written P
+        if (JOINED) zero_cols<2 * D / W::kWgs>(c.tmem + kTDV + 2 * D / W::kWgs * w + lane_off);
         bool ok = true;
         for (int it = 0; it < iters; ++it) {
             if (!__all_sync(kFull, tc::mbar_wait(c.bar(kS), it & 1, c.abort_flag))) { ok = false; break; }
@@ -796,13 +981,13 @@ static_assert(kSmem <= 232448, "shared memory budget");
 constexpr uint32_t kTS = 0, kTDP = 128, kTDQ = 256, kTDS = 384;
 }  // namespace dq
 
-template <int D, bool PARTS>
+template <int D, bool PARTS, bool JOINED>
 __device__ __forceinline__ void dq_tile(const BwdMaps& m, const BwdParams& p, unsigned char* smem_raw, int x, int pair, int part) {
     using namespace dq;
     using W = Warps<D>;
     const int z = x / p.g;
-    int grp, qlo, qn;
-    if (!find_tile(p.qtile, z, p.q_tiles, p.N, pair, grp, qlo, qn)) return;
+    int grp, qlo, qn, split;
+    if (!find_tile(p.qtile, z, p.q_tiles, p.N, pair, grp, qlo, qn, split)) return;
     const int2* list = p.klist + ((long long)z * p.Gq + grp) * p.kcap;
     // this CTA's share of the key tiles
     const int all = p.kcnt ? p.kcnt[(long long)z * p.Gq + grp] : (p.N + kTile - 1) / kTile;
@@ -825,7 +1010,8 @@ __device__ __forceinline__ void dq_tile(const BwdMaps& m, const BwdParams& p, un
     if (c.warp == W::kTma) {
         int nland = 0, nk = 0, nv = 0;
         for (int t = 0; t < nt; ++t) {
-            const int2 e = tile(t);
+            int2 e = tile(t);
+            if (JOINED) e.y &= 255;
             const int sk = t % kKStages, sv = t % kVStages, row = z * p.N + e.x;
             if (t >= kKStages && !__all_sync(kFull, tc::mbar_wait(c.bar(kKe + sk), (t / kKStages - 1) & 1, c.abort_flag))) break;
             if (!load_tile_zeroed<D>(c, c.base + kOffK + sk * 2 * kRegion, &m.k, kKf + sk, kLand, nland, row, e.y)) break;
@@ -860,11 +1046,18 @@ __device__ __forceinline__ void dq_tile(const BwdMaps& m, const BwdParams& p, un
             tc::commit_go(c.bar(kVe + t % kVStages), go);
             return true;
         };
+        const Lanes lanes(split);
+        uint32_t off[4] = {};
+        int cls = JOINED && nt > 0 ? tile(0).y >> 8 : 0;
         bool ok = nt > 0 && wait(kQO, 0) && issue_S(0) && issue_dP(0);
         for (int t = 0; ok && t < nt; ++t) {
+            if (JOINED) {
+                lanes.off(cls, off);
+                if (t + 1 < nt) cls = tile(t + 1).y >> 8;
+            }
             if (t + 1 < nt && !(wait(kSread, t) && issue_S(t + 1) && wait(kDPread, t) && issue_dP(t + 1))) break;
             if (!wait(kDS, t)) break;
-            mma_sums<D>(c.tmem + kTDQ, c.tmem + kTDS, k(t), t > 0, go);
+            mma_sums<D, JOINED>(c.tmem + kTDQ, c.tmem + kTDS, k(t), off, t > 0, go);
             tc::commit_go(c.bar(kKe + t % kKStages), go);
             tc::commit_go(c.bar(kDSfree), go);
         }
@@ -880,9 +1073,10 @@ __device__ __forceinline__ void dq_tile(const BwdMaps& m, const BwdParams& p, un
         const float nl = r < qn ? p.nlse2[row] : -INFINITY, nd = r < qn ? p.nD[row] : 0.f;
         const uint64_t cc = pk2(p.scale_log2, p.scale_log2), nl2 = pk2(nl, nl), nd2 = pk2(nd, nd);
         bool ok = true;
+        if (JOINED && w < 2) zero_cols<D / 2>(c.tmem + kTDQ + D / 2 * w + lane_off);
         int valid_next = nt > 0 ? tile(0).y : 0;
         for (int t = 0; t < nt; ++t) {
-            const int valid = valid_next;
+            const int valid = JOINED ? valid_next & 255 : valid_next;
             if (t + 1 < nt) valid_next = tile(t + 1).y;
             if (!__all_sync(kFull, tc::mbar_wait(c.bar(kS), t & 1, c.abort_flag))) { ok = false; break; }
             tc::fence_after_sync();
@@ -952,7 +1146,7 @@ __device__ __forceinline__ void dq_tile(const BwdMaps& m, const BwdParams& p, un
 template <int D>
 constexpr int kSmemBytes = kv::Layout<D>::kSmem > dq::kSmem ? kv::Layout<D>::kSmem : dq::kSmem;
 
-template <int D, bool PARTS>
+template <int D, bool PARTS, bool JOINED>
 __global__ void __launch_bounds__(Warps<D>::kThreads, 1) bwd_kernel(const __grid_constant__ BwdMaps m, const __grid_constant__ BwdParams p) {
     extern __shared__ unsigned char smem_raw[];
     // a CTA that timed out earlier in this launch (or call) makes the rest return at once
@@ -960,10 +1154,10 @@ __global__ void __launch_bounds__(Warps<D>::kThreads, 1) bwd_kernel(const __grid
     const int b = blockIdx.x, early = b - p.kv_first;
     if (early < 0 || (early >= p.q_early && b < p.kv_blocks + p.q_early)) {
         const int i = early < 0 ? b : b - p.q_early, t = PARTS ? i / p.kv_parts : i;
-        dkv_tile<D, PARTS>(m, p, smem_raw, t / p.kv_tiles, t % p.kv_tiles, PARTS ? i % p.kv_parts : 0);
+        dkv_tile<D, PARTS, JOINED>(m, p, smem_raw, t / p.kv_tiles, t % p.kv_tiles, PARTS ? i % p.kv_parts : 0);
     } else {
         const int i = early < p.q_early ? early : b - p.kv_blocks, t = PARTS ? i / p.q_parts : i;
-        dq_tile<D, PARTS>(m, p, smem_raw, t / p.q_tiles, t % p.q_tiles, PARTS ? i % p.q_parts : 0);
+        dq_tile<D, PARTS, JOINED>(m, p, smem_raw, t / p.q_tiles, t % p.q_tiles, PARTS ? i % p.q_parts : 0);
     }
 }
 
@@ -1025,10 +1219,11 @@ BwdLayout bwd_layout(int P, int g, int N, int d, int Gq, int Gk, const BwdParts&
         // the runs of a list are disjoint: at most N / 128 full tiles and one ragged tile per group
         l.kcap = (int)(tiles + Gk);
         l.qcap = (int)(tiles + Gq);
-        l.klist = take((size_t)P * Gq * l.kcap * sizeof(int2));
-        l.qlist = take((size_t)P * Gk * l.qcap * sizeof(int2));
-        l.kcnt = take((size_t)P * Gq * sizeof(int32_t));
-        l.qcnt = take((size_t)P * Gk * sizeof(int32_t));
+        const size_t lists = (size_t)P * (parts.joined ? 2 : 1);
+        l.klist = take(lists * Gq * l.kcap * sizeof(int2));
+        l.qlist = take(lists * Gk * l.qcap * sizeof(int2));
+        l.kcnt = take(lists * Gq * sizeof(int32_t));
+        l.qcnt = take(lists * Gk * sizeof(int32_t));
         l.qtile = take((size_t)P * l.qcap * sizeof(int4));
         l.ktile = take((size_t)P * l.kcap * sizeof(int4));
     }
@@ -1069,12 +1264,20 @@ cudaError_t launch_bwd(const AttnBwdArgs& a, cudaStream_t s) {
         lp.q_tiles = p.q_tiles; lp.kv_tiles = p.kv_tiles;
         lp.status = a.status;
         lp.kcap = l.kcap; lp.qcap = l.qcap; lp.P = a.P; lp.N = a.N; lp.Gq = a.Gq; lp.Gk = a.Gk;
-        list_blocks = (int)(((long long)a.P * (a.Gq + a.Gk + 2) * 32 + 255) / 256);
+        lp.g = a.g; lp.joined = a.parts.joined;
+        const long long warps = (long long)a.P * (a.parts.joined ? 2 * (a.Gq + a.Gk) : a.Gq + a.Gk + 2);
+        list_blocks = (int)((warps * 32 + 255) / 256);
+        if (a.parts.joined) {
+            bwd_lists_kernel<<<list_blocks, 256, 0, s>>>(lp);
+            const cudaError_t e = cudaGetLastError();
+            if (e != cudaSuccess) return e;
+            list_blocks = 2 * a.P;
+        }
         p.qperm = a.qperm; p.kperm = a.kperm;
         p.klist = lp.klist; p.qlist = lp.qlist; p.kcnt = lp.kcnt; p.qcnt = lp.qcnt;
         p.qtile = lp.qtile; p.ktile = lp.ktile;
         p.kcap = l.kcap; p.qcap = l.qcap;
-        p.Gq = a.Gq; p.Gk = a.Gk;
+        p.Gq = a.parts.joined ? 2 * a.Gq : a.Gq; p.Gk = a.parts.joined ? 2 * a.Gk : a.Gk;
     }
     const long long row_blocks = (rows * (D / 8) + 255) / 256;
     bwd_prepare_kernel<D><<<(unsigned)(list_blocks + row_blocks), 256, 0, s>>>(
@@ -1091,11 +1294,12 @@ cudaError_t launch_bwd(const AttnBwdArgs& a, cudaStream_t s) {
     p.kv_first = both ? p.kv_blocks - a.parts.kv_late : p.kv_blocks;
     p.q_early = both ? a.parts.q_early : 0;
     const bool parts = p.kv_parts > 1 || p.q_parts > 1;
-    const auto kernel = parts ? bwd_kernel<D, true> : bwd_kernel<D, false>;
-    if (!(*a.attributes & 1 << parts)) {
+    const auto kernel = parts ? bwd_kernel<D, true, false> : a.parts.joined ? bwd_kernel<D, false, true> : bwd_kernel<D, false, false>;
+    const int bit = 1 << (parts ? 1 : a.parts.joined ? 2 : 0);
+    if (!(*a.attributes & bit)) {
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes<D>);
         if (e != cudaSuccess) return e;
-        *a.attributes |= 1 << parts;
+        *a.attributes |= bit;
     }
     kernel<<<(unsigned)blocks, Warps<D>::kThreads, kSmemBytes<D>, s>>>(m, p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
@@ -1137,12 +1341,15 @@ struct BwdModel {
     }
 };
 
-BwdParts attn_bwd_parts(int P, int g, int N, int d, bool sparse, int sms) {
-    BwdParts best = {1, 1, 0, 0};
+BwdParts attn_bwd_parts(int P, int g, int N, int d, int Gq, int Gk, bool sparse, int sms) {
+    BwdParts best = {1, 1, 0, 0, false};
     const double tiles = (N + kTile - 1) / kTile;
     // of a route neither the density nor the groups' sizes are known here: a quarter of the keys, and
     // a quarter more tiles than whole ones
     const double len = sparse ? ceil(tiles / 4) : tiles, ctas = sparse ? ceil(1.25 * tiles) : tiles;
+    // Joined tiles take a launch more. They pay where the tiles fill the SMs, and where groups have some rows.
+    auto joined = [&](const BwdParts& b) { return sparse && b.kv == 1 && b.q == 1 && P * (tiles + Gk) > sms && N >= 32 * max(Gq, Gk); };
+    best.joined = joined(best);
     if (ctas * P > 8.0 * sms) return best;
     static const int kChoices[] = {1, 2, 3, 4, 6, 8, 12, 16};
     double best_t = 1e30;
@@ -1155,9 +1362,10 @@ BwdParts attn_bwd_parts(int P, int g, int N, int d, bool sparse, int sms) {
             if (kv > 1 || q > 1) t += 2.5 + 2 * mb / 4;
             if (t < best_t * 0.97) {      // a gain below the model's error is none
                 best_t = t;
-                best = {kv, q, 0, 0};
+                best = {kv, q, 0, 0, false};
             }
         }
+    best.joined = joined(best);
     // The order, for equal streams: m SMs turn to dQ before their last CTA of dK and dV, m others run one
     // more of those (12 heads, 4096 tokens: 277 -> 271 us with m = 28; 16 on 4 heads, 2 x 2311: 257 -> 252 with
     // 32). Here the times are those of steady tiles and of whole CTAs, by clock reads in long launches.
@@ -1181,7 +1389,7 @@ size_t attn_bwd_workspace(int P, int g, int N, int d, int Gq, int Gk, const BwdP
     return bwd_layout(P, g, N, d, Gq, Gk, parts, sparse).bytes;
 }
 
-int attn_bwd_launches(const AttnBwdArgs& a) { return 2 + ((a.dK && a.parts.kv > 1) || (a.dQ && a.parts.q > 1)); }
+int attn_bwd_launches(const AttnBwdArgs& a) { return 2 + (a.rowptr && a.parts.joined) + ((a.dK && a.parts.kv > 1) || (a.dQ && a.parts.q > 1)); }
 
 cudaError_t launch_attn_bwd(const AttnBwdArgs& a, cudaStream_t s) {
     return a.d == 128 ? launch_bwd<128>(a, s) : a.d == 64 ? launch_bwd<64>(a, s) : cudaErrorInvalidValue;

@@ -191,8 +191,9 @@ cudaError_t launch_attn_probe(const bf16* Q, const bf16* K, const bf16* V, const
 struct BwdParts {
     int kv, q;                           // CTAs that share the stream of a dK/dV tile, of a dQ tile
     int kv_late, q_early;                // CTAs of dK/dV that are launched after so many of dQ
+    bool joined;                         // a tile may hold rows of two neighbouring groups
 };
-BwdParts attn_bwd_parts(int P, int g, int N, int d, bool sparse, int sms);
+BwdParts attn_bwd_parts(int P, int g, int N, int d, int Gq, int Gk, bool sparse, int sms);
 struct AttnBwdArgs {
     const bf16 *Q, *K, *V, *O, *dO;
     const float* lse;

@@ -195,6 +195,17 @@ __device__ __forceinline__ void mma_f16_ts_go(uint32_t d_tmem, uint32_t a_tmem, 
         "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(go)
         : "memory");
 }
+// The same, leaving the accumulator's lanes whose bit in `off` (32 lanes a word) is set as they are.
+__device__ __forceinline__ void mma_f16_ts_off_go(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                                  const uint32_t (&off)[4], uint32_t accumulate, uint32_t go) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %8, 0;\n\t"
+        "setp.ne.b32 q, %9, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, {%4, %5, %6, %7}, p;\n\t}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(off[0]), "r"(off[1]), "r"(off[2]), "r"(off[3]), "r"(accumulate), "r"(go)
+        : "memory");
+}
 __device__ __forceinline__ void commit_go(uint32_t bar, uint32_t go) {
     asm volatile(
         "{\n\t.reg .pred q;\n\t"

@@ -129,6 +129,113 @@ def test_blocksparse_gradients(case):
     check_gradients(got, _to_original(backward_reference(Q, K, V, O, lse, dO, masks), t, r), f"sparse {case}")
 
 
+def _routed_by(keep, seed, P, N, empty=0):
+    g = torch.Generator().manual_seed(seed)
+    _, Gq, Gk = keep.shape
+    rowptr, kg = csr(keep)
+    qoff = torch.stack([random_groups(g, N, Gq, empty) for _ in range(P)])
+    koff = torch.stack([random_groups(g, N, Gk, empty) for _ in range(P)])
+    perm = lambda: torch.stack([torch.randperm(N, generator=g) for _ in range(P)]).to(torch.int32)  # noqa: E731
+    masks = [pair_mask(keep[z], qoff[z], koff[z]).cuda() for z in range(P)]
+    return {k: v.cuda() for k, v in dict(qperm=perm(), kperm=perm(), qoff=qoff, koff=koff, rowptr=rowptr, kg=kg).items()}, masks
+
+
+# Enough tiles to fill the SMs: tiles may then hold rows of two groups. Neighbours keep much the same groups
+# (band: those up to `share` of all away), or groups drawn one by one.
+JOINED = [
+    # B, Hq, Hkv, N, d, Gq, Gk, band, share, empty groups
+    (2, 8, 4, 900, 128, 24, 20, True, 0.2, 2), (2, 8, 4, 900, 128, 24, 20, False, 0.3, 2),
+    (1, 12, 12, 1300, 64, 40, 30, True, 0.3, 3), (1, 12, 12, 1300, 64, 40, 30, False, 0.1, 0),
+    (1, 10, 10, 517, 128, 2, 16, False, 1.0, 0), (2, 16, 8, 700, 64, 20, 21, False, 0.0, 4),
+    (1, 40, 20, 1030, 128, 32, 32, True, 0.06, 16), (1, 24, 24, 2049, 128, 9, 60, True, 0.15, 0),
+]
+
+
+@gpu
+@pytest.mark.parametrize("case", JOINED, ids=str)
+def test_tiles_of_two_groups(case):
+    _need_gpu()
+    B, Hq, Hkv, N, d, Gq, Gk, band, share, empty = case
+    P, r = B * Hkv, Hq // Hkv
+    at = lambda G: (torch.arange(G) + 0.5) / G  # noqa: E731
+    keep = ((at(Gq)[:, None] - at(Gk)).abs() < share).expand(P, Gq, Gk) if band else \
+        torch.rand((P, Gq, Gk), generator=torch.Generator().manual_seed(N)) < share
+    Q, K, V, dO = _inputs(5 * N + d, B, Hq, Hkv, N, d)
+    t, masks = _routed_by(keep, N + Gq, P, N, empty)
+    part, route = _structs(t)
+    O, lse = forward_reference(Q, K, V, masks)
+    O, lse = O.bfloat16(), lse.float()
+    with _handle(B, Hq, Hkv, N, d, Gk, Gq) as h:
+        ws = torch.full((h.attn_bwd_workspace_bytes(),), 0x7B, dtype=torch.uint8, device="cuda")
+        got = h.blocksparse_attn_bwd(Q, K, V, part, route, O, lse, dO, workspace=ws)
+        dq = h.blocksparse_attn_bwd(Q, K, V, part, route, O, lse, dO, need_dkv=False)[0]
+        _, dk, dv = h.blocksparse_attn_bwd(Q, K, V, part, route, O, lse, dO, need_dq=False)
+        out = [torch.zeros_like(x) for x in got]
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            h.blocksparse_attn_bwd(Q, K, V, part, route, O, lse, dO, *out, workspace=ws)
+        graph.replay()
+        torch.cuda.synchronize()
+        del graph
+        assert h.device_status() == 0
+    assert all(torch.equal(a, b) for a, b in zip(got, (dq, dk, dv))) and all(torch.equal(a, b) for a, b in zip(got, out))
+    check_gradients(got, _to_original(backward_reference(Q, K, V, O, lse, dO, masks), t, r), f"joined {case}")
+
+
+@gpu
+def test_non_finite_rows_stay_apart_in_a_tile_of_two_groups():
+    _need_gpu()
+    B, Hq, Hkv, N, d = 5, 10, 5, 300, 128
+    P = B * Hkv
+    Q, K, V, dO = _inputs(23, B, Hq, Hkv, N, d)
+    off = torch.tensor([[0, 100, 170, 300]], dtype=torch.int32).repeat(P, 1)      # the last two share a tile
+    keep = torch.eye(3, dtype=torch.bool).expand(P, 3, 3)
+    rowptr, kg = csr(keep)
+    ident = torch.arange(N, dtype=torch.int32).repeat(P, 1)
+    t = {k: v.cuda() for k, v in dict(qperm=ident, kperm=ident, qoff=off, koff=off, rowptr=rowptr, kg=kg).items()}
+    masks = [pair_mask(keep[0], off[0], off[0]).cuda()] * P
+    O, lse = forward_reference(Q, K, V, masks)
+    O, lse = O.bfloat16(), lse.float()
+    part, route = _structs(t)
+    with _handle(B, Hq, Hkv, N, d, 3, 3) as h:
+        clean = h.blocksparse_attn_bwd(Q, K, V, part, route, O, lse, dO)
+        for rows in (slice(0, 100), slice(100, 170), slice(170, 300)):
+            for bad in (math.nan, math.inf):
+                q, k, v, do, o, l = (x.clone() for x in (Q, K, V, dO, O, lse))
+                for x in (q, k, v, do, o, l):
+                    x[:, :, rows] = bad
+                got = h.blocksparse_attn_bwd(q, k, v, part, route, o, l, do)
+                for a, b in zip(got, clean):
+                    a, b = a.clone(), b.clone()
+                    a[:, :, rows] = b[:, :, rows] = 0
+                    assert torch.equal(a, b)
+
+
+@gpu
+def test_out_of_range_ids_are_reported_with_tiles_of_two_groups():
+    _need_gpu()
+    B, Hq, Hkv, N, d, G = 4, 10, 10, 400, 64, 4
+    Q, K, V, dO = _inputs(4, B, Hq, Hkv, N, d)
+    t, masks = _routed(4, B * Hkv, N, G, G, 1.0)
+    O, lse = forward_reference(Q, K, V, masks)
+    args = (O.bfloat16(), lse.float(), dO)
+    with _handle(B, Hq, Hkv, N, d, G, G) as h:
+        want = h.blocksparse_attn_bwd(Q, K, V, *_structs(t), *args)
+        torch.cuda.synchronize()
+        assert h.device_status() == 0
+        for name, at, value in (("kg", (3, 1), G), ("kg", (0, 2), -3), ("rowptr", (39, 2), 10 ** 6), ("rowptr", (1, 1), -5),
+                                ("koff", (0, 2), N + 5), ("qoff", (7, 1), -7), ("kg", (0, 1), 0), ("kg", (0, 0), G - 1),
+                                ("qoff", (0, 0), 3), ("koff", (9, G), N - 1), ("koff", (2, 2), 0), ("qoff", (2, 1), 2 ** 31 - 1)):
+            bad = {k: v.clone() for k, v in t.items()}
+            bad[name][at] = value
+            h.blocksparse_attn_bwd(Q, K, V, *_structs(bad), *args)
+            torch.cuda.synchronize()
+            assert h.device_status() == 6, name
+        got = h.blocksparse_attn_bwd(Q, K, V, *_structs(t), *args)
+        torch.cuda.synchronize()
+        assert h.device_status() == 0 and all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 @gpu
 @pytest.mark.parametrize("amp", [1e-3, 4.0, 12.0])
 def test_flat_and_peaked_rows(amp):
