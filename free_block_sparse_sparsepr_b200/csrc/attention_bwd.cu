@@ -31,7 +31,8 @@ struct BwdParams {
     const int32_t *qperm, *kperm;           // output row of each position (null: the position itself)
     const int2 *klist, *qlist;              // kept key tiles of each query group (or two), query tiles of each key group
     const int32_t *kcnt, *qcnt;             // their numbers
-    const int4 *qtile, *ktile;              // [P][q_tiles], [P][kv_tiles]: list, first row, rows of each tile (0: none), split
+    const int4 *qtile, *ktile;              // [P][q_tiles], [P][kv_tiles]: list, first row, rows of each tile (0: none); joined:
+                                            // rows of the first group (0: of one group) << 8, and the list's length
     int kcap, qcap;                         // list entries per group
     int* status;
     long long krows, qrows;                 // P N, P g N
@@ -131,14 +132,14 @@ struct Runs {
     }
 };
 
-// Whether the kept ids kept[r.x .. r.y) hold `id`.
-__device__ __forceinline__ bool holds(const int32_t* kept, int2 r, int id) {
-    int b = r.x, e = r.y;
-    while (b < e) {
-        const int m = (b + e) >> 1;
-        if (kept[m] < id) b = m + 1; else e = m;
+// Whether the ascending ids kept[r.x .. r.y) hold `id`; the next search, for an id above, starts at `r.x`.
+__device__ __forceinline__ bool holds(const int32_t* kept, int2& r, int id) {
+    int e = r.y;
+    while (r.x < e) {
+        const int m = (r.x + e) >> 1;
+        if (kept[m] < id) r.x = m + 1; else e = m;
     }
-    return b < r.y && kept[b] == id;
+    return r.x < r.y && kept[r.x] == id;
 }
 
 __device__ void tile_lists(const ListParams& l, int wid, int lane) {
@@ -225,9 +226,12 @@ __device__ void tile_lists(const ListParams& l, int wid, int lane) {
                 int2 b = make_int2(0, 0);
                 int cls = 0;
                 if (k < others) {
-                    const int2 r = rows ? r0 : row_range(k);
-                    cls = holds(kept, r, rows ? k : own) | holds(kept, rows ? r1 : r, rows ? k : next) << 1;
-                    if (cls) b = bounds(k);
+                    b = bounds(k);
+                    int2 r = rows ? r0 : row_range(k), other = r1;
+                    cls = holds(kept, r, rows ? k : own);
+                    if (!rows) other = make_int2(r.x, min(r.y, r.x + next - own + 1));      // ids ascend
+                    cls |= holds(kept, other, rows ? k : next) << 1;
+                    if (!cls) b = make_int2(0, 0);
                 }
                 runs.add(b.x, b.y, cls);
             }
@@ -246,8 +250,9 @@ __device__ void tile_lists(const ListParams& l, int wid, int lane) {
                         bad = true;
                         grp = -1;
                     }
-                } else if (holds(kept, row_range(c), own)) {
-                    grp = c;
+                } else {
+                    int2 r = row_range(c);
+                    if (holds(kept, r, own)) grp = c;
                 }
                 if (grp >= 0) b = bounds(grp);
             }
@@ -259,13 +264,14 @@ __device__ void tile_lists(const ListParams& l, int wid, int lane) {
     if (__any_sync(kFull, bad || runs.bad) && lane == 0) set_status(status, kDevBounds);
 }
 
-// The cut of one side of one KV head (z = i / 2; keys where i is odd) into tiles of one or two groups, by one
-// warp. Four ways to deal with a group's last rows, r < 128 of them: a tile of their own; joined with the next
+// The cut of one side of one KV head (z = i / 2; keys where i is odd) into tiles of one or two groups, by four
+// warps. Four ways to deal with a group's last rows, r < 128 of them: a tile of their own; joined with the next
 // group's own last rows where both fit a tile (a tile fewer, and the list no longer than both), those moved to
-// its front; the same filled up; filled up with the next group's first rows always. The lanes 0 to 3 walk one
-// each and count streamed tiles, 3.5 more for a CTA's start and end; the cheapest is written.
-__device__ void joined_tiles(const ListParams& l, int i, int lane) {
-    __shared__ int s_lo[kMaxGroups], s_n[kMaxGroups], s_one[kMaxGroups], s_two[kMaxGroups];
+// its front; the same filled up; filled up with the next group's first rows always. Each warp walks one
+// and counts streamed tiles, 3.5 more for a CTA's start and end; the cheapest is written.
+__device__ void joined_tiles(const ListParams& l, int i, int warp, int lane) {
+    __shared__ unsigned long long s_cost[4];
+    __shared__ int4 s_group[kMaxGroups];         // first row, rows, streamed tiles alone and with the next group
     __shared__ unsigned short s_id[kMaxGroups];
     const int z = i >> 1, keys = i & 1, G = keys ? l.Gk : l.Gq, N = l.N;
     const int32_t* off = keys ? l.koff + (long long)z * (G + 1) : l.qoff + (long long)z * (G + 1);
@@ -274,7 +280,7 @@ __device__ void joined_tiles(const ListParams& l, int i, int lane) {
     int4* out = (keys ? l.ktile : l.qtile) + (long long)z * cap;
     bool bad = off[0] != 0 || off[G] != N;       // rows that no group holds would get no gradient
     int m = 0;                                   // groups that are not empty
-    for (int g0 = 0; g0 < G; g0 += 32) {
+    for (int g0 = 0; g0 < G; g0 += 32) {         // (every warp counts them, the first keeps them)
         const int grp = g0 + lane;
         int lo = 0, hi = 0;
         if (grp < G) {
@@ -286,50 +292,52 @@ __device__ void joined_tiles(const ListParams& l, int i, int lane) {
             }
         }
         const unsigned some = __ballot_sync(kFull, hi > lo);
-        if (hi > lo) {
+        if (hi > lo && warp == 0) {
             const int at = m + __popc(some & ((1u << lane) - 1));
-            s_lo[at] = lo;
-            s_n[at] = hi - lo;
-            s_one[at] = cnt[grp];
-            s_two[at] = cnt[G + grp];
+            s_group[at] = make_int4(lo, hi - lo, cnt[grp], cnt[G + grp]);
             s_id[at] = (unsigned short)grp;
         }
         m += __popc(some);
     }
-    __syncwarp();
-    // calls tile(list, first row, rows, split, streamed tiles)
+    tc::named_bar_sync(1, 128);
+    // calls tile(list, first row, rows, split, streamed tiles, number of such tiles after one another)
     auto walk = [&](int mode, auto tile) {
-        for (int j = 0, o = 0; j < m;) {         // o rows of group j are in tiles
-            const int n = s_n[j], rest = n - o, lo = s_lo[j] + o;
+        int o = 0;                               // rows of the group that are in tiles
+        int4 e = s_group[0];
+        for (int j = 0; j < m;) {
+            const int id = s_id[j], lo = e.x + o, rest = e.y - o, whole = rest / kTile, r = rest % kTile;
+            const int4 next = s_group[min(j + 1, m - 1)];
+            if (whole) tile(id, lo, kTile, 0, e.z, whole);
+            const int at = lo + whole * kTile;
             int take = 0;
-            if (rest < kTile && mode > 0 && j + 1 < m && s_lo[j + 1] == s_lo[j] + n) {
-                const int next = s_n[j + 1], room = kTile - rest, last = (next - 1) % kTile + 1;
-                take = mode == 3 ? min(room, next) : last > room ? 0 : mode == 2 ? min(room, next) : last;
+            if (r && mode > 0 && j + 1 < m && next.x == at + r) {
+                const int room = kTile - r, last = (next.y - 1) % kTile + 1;
+                take = mode == 3 ? min(room, next.y) : last > room ? 0 : mode == 2 ? min(room, next.y) : last;
             }
-            if (take > 0) tile(G + s_id[j], lo, rest + take, rest, s_two[j]);
-            else tile(s_id[j], lo, min(rest, kTile), 0, s_one[j]);
-            if (rest > kTile) {
-                o += kTile;
-            } else {
+            if (r) tile(take ? G + id : id, at, r + take, take ? r : 0, take ? e.w : e.z, 1);
+            ++j;
+            o = take;
+            e = next;
+            if (take && take == next.y) {
                 ++j;
-                o = take;
-                if (take > 0 && take == s_n[j]) {
-                    ++j;
-                    o = 0;
-                }
+                o = 0;
+                e = s_group[min(j, m - 1)];
             }
         }
     };
     const int heads = keys ? l.g : 1;
     unsigned long long cost = 0;
-    if (lane < 4) walk(lane, [&](int, int, int, int, int streamed) { cost += 2ull * streamed * heads + 7; });
+    walk(warp, [&](int, int, int, int, int streamed, int n) { cost += n * (2ull * streamed * heads + 7); });
+    if (lane == 0) s_cost[warp] = cost;
+    tc::named_bar_sync(1, 128);
+    if (warp != 0) return;
     int mode = 0;
     for (int k = 1; k < 4; ++k)
-        if (__shfl_sync(kFull, cost, k) < __shfl_sync(kFull, cost, mode)) mode = k;
+        if (s_cost[k] < s_cost[mode]) mode = k;
     int nt = 0;
-    walk(mode, [&](int list, int lo, int rows, int split, int) {
-        if (nt < cap && lane == 0) out[nt] = make_int4(list, lo, rows, split);
-        ++nt;
+    walk(mode, [&](int list, int lo, int rows, int split, int streamed, int n) {
+        for (int t = lane; t < n && nt + t < cap; t += 32) out[nt + t] = make_int4(list, lo + t * kTile, rows | split << 8, streamed);
+        nt += n;
     });
     if (nt > cap) bad = true;                    // more tiles than disjoint groups can have
     for (int t = nt + lane; t < cap; t += 32) out[t] = make_int4(0, 0, 0, 0);
@@ -337,13 +345,13 @@ __device__ void joined_tiles(const ListParams& l, int i, int lane) {
 }
 
 // The lists (blocks before `list_blocks`) and the rows' terms (the others) in one launch; the joined tiles
-// read the lists, so then these have a launch of their own and the tiles (a warp a block) take their place.
+// read the lists, so then these have a launch of their own and the tiles take their place.
 template <int D>
 __global__ void __launch_bounds__(256) bwd_prepare_kernel(const ListParams l, int list_blocks, const uint4* O, const uint4* dO,
                                                           const float* lse, float* nlse2, float* nD, long long rows) {
     if ((int)blockIdx.x < list_blocks) {
         if (!l.joined) tile_lists(l, (blockIdx.x * blockDim.x + threadIdx.x) >> 5, threadIdx.x & 31);
-        else if (threadIdx.x < 32) joined_tiles(l, blockIdx.x, threadIdx.x);
+        else if (threadIdx.x < 128) joined_tiles(l, blockIdx.x, threadIdx.x >> 5, threadIdx.x & 31);
         return;
     }
     row_terms<D>(O, dO, lse, nlse2, nD, rows, (long long)(blockIdx.x - list_blocks) * blockDim.x + threadIdx.x);
@@ -666,15 +674,16 @@ __device__ __forceinline__ bf16* out_row(bf16* base, const int32_t* perm, long l
     return base + (head * N + row) * D;
 }
 
-// Tile `pair` of one side: rows [lo, lo + n) that stream list `grp`, the first `split` of them of a group of
-// their own; false past the last tile. (A table: a
+// Tile `pair` of one side: rows [lo, lo + n) that stream list `grp`; joined: its length `count`, and the first
+// `split` rows' own group. False past the last tile. (A table: a
 // search of the group offsets costs a CTA some eight reads of memory one after another.)
-__device__ __forceinline__ bool find_tile(const int4* table, int z, int tiles, int N, int pair, int& grp, int& lo, int& n, int& split) {
+__device__ __forceinline__ bool find_tile(const int4* table, int z, int tiles, int N, int pair, int& grp, int& lo, int& n, int& split, int& count) {
     const int4 e = table ? __ldg(table + (long long)z * tiles + pair) : make_int4(0, pair * kTile, min(kTile, N - pair * kTile), 0);
     grp = e.x;
     lo = e.y;
-    n = e.z;
-    split = e.w;
+    n = e.z & 255;
+    split = e.z >> 8;
+    count = e.w;
     return n > 0;
 }
 
@@ -728,10 +737,10 @@ __device__ __forceinline__ void dkv_tile(const BwdMaps& m, const BwdParams& p, u
     constexpr int kOffExt = L::kOffExt, kOffOne = L::kOffOne, kOffBar = L::kOffBar;
     constexpr int kOf = L::kOf, kQe = L::kQe, kOe = L::kOe, kS = L::kS, kDP = L::kDP, kDone = L::kDone, kLand = L::kLand, kSread = L::kSread,
                   kDPread = L::kDPread, kP = L::kP, kDS = L::kDS, kBars = L::kBars;
-    int grp, klo, kn, split;
-    if (!find_tile(p.ktile, z, p.kv_tiles, p.N, pair, grp, klo, kn, split)) return;
+    int grp, klo, kn, split, count;
+    if (!find_tile(p.ktile, z, p.kv_tiles, p.N, pair, grp, klo, kn, split, count)) return;
     const int2* list = p.qlist + ((long long)z * p.Gk + grp) * p.qcap;
-    const int nt = p.qcnt ? p.qcnt[(long long)z * p.Gk + grp] : (p.N + kTile - 1) / kTile;
+    const int nt = JOINED ? count : p.qcnt ? p.qcnt[(long long)z * p.Gk + grp] : (p.N + kTile - 1) / kTile;
     // this CTA's share of the (query head, query tile) stream
     const long long all = (long long)nt * p.g;
     const int first = PARTS ? (int)(all * part / p.kv_parts) : 0;
@@ -893,6 +902,12 @@ __device__ __forceinline__ void dkv_tile(const BwdMaps& m, const BwdParams& p, u
         // the first sums into a lane need not be the tile's first: all start from zero, before this thread says
         // that it has written P
         if (JOINED) zero_cols<2 * D / W::kWgs>(c.tmem + kTDV + 2 * D / W::kWgs * w + lane_off);
+        // even warpgroups store dV, odd ones dK, each its share of the row's columns; many short streams: where to
+        // is read beforehand (8192 tokens x 24 heads, 22% kept: 719 us without, 705 with; dense 272 and 276)
+        constexpr int kN = D / (W::kWgs / 2);
+        const int is_dk = w & 1, col = (w >> 1) * kN;
+        auto place = [&] { return out_row<D>(is_dk ? p.dK : p.dV, p.kperm, z, p.N, klo + r, r < kn, z, p.status); };
+        bf16* const early = JOINED ? place() : nullptr;
         bool ok = true;
         for (int it = 0; it < iters; ++it) {
             if (!__all_sync(kFull, tc::mbar_wait(c.bar(kS), it & 1, c.abort_flag))) { ok = false; break; }
@@ -945,11 +960,8 @@ __device__ __forceinline__ void dkv_tile(const BwdMaps& m, const BwdParams& p, u
             tc::fence_before_sync();
             tc::mbar_arrive(c.bar(kDS));
         }
-        // even warpgroups store dV, odd ones dK, each its share of the row's columns
         if (__all_sync(kFull, ok && tc::mbar_wait(c.bar(kDone), 0, c.abort_flag))) {
             tc::fence_after_sync();
-            constexpr int kN = D / (W::kWgs / 2);
-            const int is_dk = w & 1, col = (w >> 1) * kN;
             const uint32_t acc = c.tmem + (is_dk ? kTDK : kTDV) + col + lane_off;
             // the streamed tiles have all been used: their buffers take the rows
             unsigned char* stage = c.sbase + kOffBuf + c.warp * (32 * kN * 4);
@@ -958,7 +970,7 @@ __device__ __forceinline__ void dkv_tile(const BwdMaps& m, const BwdParams& p, u
                 const long long row = (part * 2 + is_dk) * p.krows + (long long)z * p.N + klo + r;
                 store_acc_rows<kN, float>(acc, stage, c.lane, 1.f, iters == 0, r < kn ? p.kv_part + row * D + col : nullptr);
             } else {
-                bf16* out = out_row<D>(is_dk ? p.dK : p.dV, p.kperm, z, p.N, klo + r, r < kn, z, p.status);
+                bf16* out = JOINED ? early : place();
                 store_acc_rows<kN, bf16>(acc, stage, c.lane, is_dk ? p.scale : 1.f, iters == 0, out ? out + col : nullptr);
             }
         }
@@ -986,11 +998,11 @@ __device__ __forceinline__ void dq_tile(const BwdMaps& m, const BwdParams& p, un
     using namespace dq;
     using W = Warps<D>;
     const int z = x / p.g;
-    int grp, qlo, qn, split;
-    if (!find_tile(p.qtile, z, p.q_tiles, p.N, pair, grp, qlo, qn, split)) return;
+    int grp, qlo, qn, split, count;
+    if (!find_tile(p.qtile, z, p.q_tiles, p.N, pair, grp, qlo, qn, split, count)) return;
     const int2* list = p.klist + ((long long)z * p.Gq + grp) * p.kcap;
     // this CTA's share of the key tiles
-    const int all = p.kcnt ? p.kcnt[(long long)z * p.Gq + grp] : (p.N + kTile - 1) / kTile;
+    const int all = JOINED ? count : p.kcnt ? p.kcnt[(long long)z * p.Gq + grp] : (p.N + kTile - 1) / kTile;
     const int first = PARTS ? (int)((long long)all * part / p.q_parts) : 0;
     const int nt = PARTS ? (int)((long long)all * (part + 1) / p.q_parts) - first : all;
     auto tile = [&](int t) {
@@ -1071,6 +1083,8 @@ __device__ __forceinline__ void dq_tile(const BwdMaps& m, const BwdParams& p, un
         const uint32_t tDS = c.tmem + kTDS + W::kCols / 2 * w + lane_off;
         const long long row = (long long)x * p.N + qlo + r;
         const float nl = r < qn ? p.nlse2[row] : -INFINITY, nd = r < qn ? p.nD[row] : 0.f;
+        auto place = [&] { return out_row<D>(p.dQ, p.qperm, x, p.N, qlo + r, r < qn, z, p.status); };
+        bf16* const early = JOINED ? place() : nullptr;      // as in the other pass
         const uint64_t cc = pk2(p.scale_log2, p.scale_log2), nl2 = pk2(nl, nl), nd2 = pk2(nd, nd);
         bool ok = true;
         if (JOINED && w < 2) zero_cols<D / 2>(c.tmem + kTDQ + D / 2 * w + lane_off);
@@ -1129,10 +1143,10 @@ __device__ __forceinline__ void dq_tile(const BwdMaps& m, const BwdParams& p, un
             unsigned char* stage = c.sbase + kOffK + c.warp * (32 * kN * 4);     // as in the other pass
             static_assert(8 * 32 * kN * 4 <= (kKStages + kVStages) * 2 * kRegion, "staging");
             if (PARTS && p.q_parts > 1) {
-                float* out = p.q_part + (part * p.qrows + (long long)x * p.N + qlo + r) * D + w * kN;
-                store_acc_rows<kN, float>(acc, stage, c.lane, 1.f, nt == 0, r < qn ? out : nullptr);
+                float* sums = p.q_part + (part * p.qrows + (long long)x * p.N + qlo + r) * D + w * kN;
+                store_acc_rows<kN, float>(acc, stage, c.lane, 1.f, nt == 0, r < qn ? sums : nullptr);
             } else {
-                bf16* out = out_row<D>(p.dQ, p.qperm, x, p.N, qlo + r, r < qn, z, p.status);
+                bf16* out = JOINED ? early : place();
                 store_acc_rows<kN, bf16>(acc, stage, c.lane, p.scale, nt == 0, out ? out + w * kN : nullptr);
             }
         }
