@@ -8,9 +8,9 @@
 // fixed order by one CTA, or by a fixed number of CTAs whose sums are joined in order (no atomics), so
 // results repeat bit for bit.
 //
-// Bound by the tensor pipe (73% of its cycles at 4096 rows, d = 128) and, in long calls, by the power cap: 12 heads x
-// 4096 rows, d = 128 take 278 us (927 TFLOP/s of 10 N^2 d a head), 24 x 8192 2.27 ms (910 TFLOP/s, the seven
-// products at 1.27 PFLOP/s), 24 x 4096 at d = 64 378 us (682 TFLOP/s).
+// Bound by the tensor pipe (74% of its cycles at 4096 rows, d = 128) and, in long calls, by the power cap: 12 heads x
+// 4096 rows, d = 128 take 266 us (969 TFLOP/s of 10 N^2 d a head), 24 x 8192 2.21 ms (932 TFLOP/s, the seven
+// products at 1.30 PFLOP/s), 24 x 4096 at d = 64 378 us (682 TFLOP/s).
 #include <math.h>
 #include <string.h>
 
@@ -90,7 +90,7 @@ __device__ __forceinline__ void row_terms(const uint4* __restrict__ O, const uin
 // each entry with the groups that keep it (1 the first, 2 the second, 3 both; two more warps per group), and
 // the sums skip the other group's lanes. Which tiles to join depends on how much the lists share: the cut is
 // chosen per KV head and side with the lists at hand (joined_tiles). 24 heads x 8192 tokens, 64 uneven groups,
-// 22% kept: the owned tiles are filled to 1.0 in place of 0.67.
+// 22% kept: the owned tiles are filled to 1.0 in place of 0.67, 690 us in place of 930; 12 x 16384 1182 and 1370.
 constexpr int kMaxGroups = 1024;            // of a side
 struct ListParams {
     const int32_t *rowptr, *kg, *qoff, *koff;
