@@ -8,6 +8,13 @@
 // fixed order by one CTA, or by a fixed number of CTAs whose sums are joined in order (no atomics), so
 // results repeat bit for bit.
 //
+// Roundings: P and dS become bf16 (2^-8 of each element at most) because the tensor cores take no fp32
+// operand, and TF32 would halve their rate. In the 2-norm against fp64 that leaves dQ at 2.5 to 3.0e-3, dK and dV at
+// 2.2 to 2.4e-3, where rounding the exact gradients to bf16 costs 1.7e-3. dQ suffers most: sum_j dS_ij = 0 takes
+// the keys' common part out of the gradient but not out of the errors. A second bf16 part of dS brings dQ to
+// 1.7e-3 for an eighth product (4096 rows, 12 heads: 17% more time; 24 x 8192: 12%). lse, D, the logits and all
+// sums are fp32.
+//
 // Bound by the tensor pipe (74% of its cycles at 4096 rows, d = 128) and, in long calls, by the power cap: 12 heads x
 // 4096 rows, d = 128 take 266 us (969 TFLOP/s of 10 N^2 d a head), 24 x 8192 2.21 ms (932 TFLOP/s, the seven
 // products at 1.30 PFLOP/s), 24 x 4096 at d = 64 378 us (682 TFLOP/s).
