@@ -553,7 +553,7 @@ class Rope:
         self._plans = {}
         import torch
 
-        self._int32 = torch.int32
+        self._int32, self._bf16 = torch.int32, torch.bfloat16
 
     @staticmethod
     def _frequencies(w, base, scaling, factor, trained, beta_fast, beta_slow):
@@ -575,7 +575,7 @@ class Rope:
         return [f / factor * s + f * (1.0 - s) for f, s in zip(freq, slow)]
 
     def _config(self, model, pos):
-        """The call's plan for this shape, strides and type, checked when first met."""
+        """The call's plan for this shape, strides and type, checked when first met, and the head-major shape."""
         key = (model.shape, model.stride(), model.dtype, pos.shape)
         c = self._plans.get(key)
         if c is None:
@@ -603,43 +603,38 @@ class Rope:
         c = RopeConfig(B, H, N, d, self.layout, axes, 1 if model.dtype == torch.float32 else 0,
                        (ctypes.c_int * 3)(*self.widths), *model.stride()[:3], N * axes if pos.dim() == 3 else 0,
                        self.amplitude, (ctypes.c_double * 64)(*self.freq))
-        return ctypes.byref(c)
+        return ctypes.byref(c), (B, H, N, d)
 
     def forward(self, x, pos, out=None, stream=None):
         """x [B, N, H, d] bf16 or fp32 (any strides of 16-byte multiples, e.g. a slice of a fused projection)
         turned by int32 positions [N, axes] or [B, N, axes]: bf16 [B, H, N, d]."""
-        import torch
-
-        cfg = self._config(x, pos)
-        B, N, H, d = x.shape
-        with _on(x.device, stream):
+        cfg, shape = self._config(x, pos)
+        dev, bf16 = x.device, self._bf16
+        with _on(dev, stream):
             if out is None:
-                out = (x.new_empty((B, H, N, d)) if x.dtype is torch.bfloat16 else      # half a microsecond less
-                       torch.empty((B, H, N, d), dtype=torch.bfloat16, device=x.device))
+                out = x.new_empty(shape) if x.dtype is bf16 else x.new_empty(shape, dtype=bf16)
             else:
-                _want("out", out, (B, H, N, d), torch.bfloat16, x.device)
+                _want("out", out, shape, bf16, dev)
             _check("sparsepr_rope", self.lib.sparsepr_rope(cfg, x.data_ptr(), pos.data_ptr(), out.data_ptr(),
-                                                           _stream_on(x.device, stream)))
+                                                           _stream_on(dev, stream)))
         return out
 
     def backward(self, dy, pos, out=None, dtype=None, stream=None):
         """Gradient dy bf16 [B, H, N, d] of forward's output -> gradient of x, [B, N, H, d] of `dtype` (bf16
         unless given) or written into `out` (any strides of 16-byte multiples whose rows do not overlap)."""
-        import torch
-
         if dy.dim() != 4 or not dy.is_cuda or out is not None and dtype not in (None, out.dtype):
             raise ValueError("dy must be [B, H, N, d] on a CUDA device, and dtype that of out")
         B, H, N, d = dy.shape
-        _want("dy", dy, (B, H, N, d), torch.bfloat16, dy.device)
-        with _on(dy.device, stream):
+        dev = dy.device
+        _want("dy", dy, (B, H, N, d), self._bf16, dev)
+        with _on(dev, stream):
             if out is None:
-                out = (dy.new_empty((B, N, H, d)) if dtype is None else
-                       torch.empty((B, N, H, d), dtype=dtype, device=dy.device))
-            elif tuple(out.shape) != (B, N, H, d) or out.device != dy.device:
-                raise ValueError(f"out: expected [{B}, {N}, {H}, {d}] on {dy.device}, got {tuple(out.shape)} on {out.device}")
-            cfg = self._config(out, pos)
+                out = dy.new_empty((B, N, H, d)) if dtype is None else dy.new_empty((B, N, H, d), dtype=dtype)
+            elif tuple(out.shape) != (B, N, H, d) or out.device != dev:
+                raise ValueError(f"out: expected [{B}, {N}, {H}, {d}] on {dev}, got {tuple(out.shape)} on {out.device}")
+            cfg, _ = self._config(out, pos)
             _check("sparsepr_rope_bwd", self.lib.sparsepr_rope_bwd(cfg, dy.data_ptr(), pos.data_ptr(), out.data_ptr(),
-                                                                   _stream_on(dy.device, stream)))
+                                                                   _stream_on(dev, stream)))
         return out
 
 
