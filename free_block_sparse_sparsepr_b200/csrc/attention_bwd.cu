@@ -400,8 +400,9 @@ struct Cta {
     __device__ __forceinline__ uint32_t bar(int i) const { return bars + 8u * (uint32_t)i; }
 };
 
+// A CTA that timed out earlier (in this launch or call) makes the rest abort at their first wait.
 template <int D, typename Count, typename Early>
-__device__ __forceinline__ Cta cta_setup(unsigned char* smem_raw, int off_bar, int nbars, Count count, Early early) {
+__device__ __forceinline__ Cta cta_setup(unsigned char* smem_raw, int off_bar, int nbars, const int* status, Count count, Early early) {
     Cta c;
     const uint32_t raw = tc::smem_addr(smem_raw);
     c.base = (raw + 1023u) & ~1023u;
@@ -413,10 +414,11 @@ __device__ __forceinline__ Cta cta_setup(unsigned char* smem_raw, int off_bar, i
     uint32_t* slot = reinterpret_cast<uint32_t*>(c.sbase + off_bar + 8 * nbars);
     c.abort_flag = reinterpret_cast<volatile int*>(slot + 1);
     if (c.warp == Warps<D>::kTma && c.lane == 0) {
+        const int before = *reinterpret_cast<const volatile int*>(status);
         for (int i = 0; i < nbars; ++i) tc::mbar_init(c.bar(i), count(i));
-        *c.abort_flag = 0;
         tc::fence_mbar_init();
         early(c);
+        *c.abort_flag = before == kDevTimeout;
     }
     if (c.warp == Warps<D>::kMma) {
         tc::tmem_alloc(tc::smem_addr(slot), kTmemCols);
@@ -753,6 +755,8 @@ __device__ __forceinline__ void dkv_tile(const BwdMaps& m, const BwdParams& p, u
     const int first = PARTS ? (int)(all * part / p.kv_parts) : 0;
     const int iters = PARTS ? (int)(all * (part + 1) / p.kv_parts) - first : (int)all;
     auto tile = [&](int t) { return p.qcnt ? list[t] : make_int2(t * kTile, min(kTile, p.N - t * kTile)); };
+    const int t0 = PARTS && nt ? first % nt : 0;
+    const int2 e0 = JOINED && iters > 0 ? tile(t0) : make_int2(0, 0);      // read while the CTA sets up
     {
         // ones under the parts of -lse (columns 0-2), or under those of -D (3-5); the halves of columns
         // 8-15 are zero everywhere
@@ -769,7 +773,7 @@ __device__ __forceinline__ void dkv_tile(const BwdMaps& m, const BwdParams& p, u
         tc::fence_proxy_async_smem();
     }
     const Cta c = cta_setup<D>(
-        smem_raw, kOffBar, kBars, [](int i) { return i >= kSread ? W::kArrivals : i >= kQf && i < kOf ? 2 : 1; },
+        smem_raw, kOffBar, kBars, p.status, [](int i) { return i >= kSread ? W::kArrivals : i >= kQf && i < kOf ? 2 : 1; },
         [&](const Cta& c) {
             tc::mbar_arrive_expect_tx(c.bar(kKV), 2 * (D / 64) * kRegion);
             for (int h = 0; h < D / 64; ++h) {
@@ -779,7 +783,7 @@ __device__ __forceinline__ void dkv_tile(const BwdMaps& m, const BwdParams& p, u
         });
 
     if (c.warp == W::kTma) {
-        int nland = 0, nq = 0, no = 0, t = PARTS && nt ? first % nt : 0, x = z * p.g + (PARTS && nt ? first / nt : 0);
+        int nland = 0, nq = 0, no = 0, t = t0, x = z * p.g + (PARTS && nt ? first / nt : 0);
         // this lane's four rows of the next tile's terms; rows past its end give P = 2^(-huge) = 0
         float nl[4], nd[4];
         auto fetch = [&](int2 e, int head) {
@@ -792,7 +796,7 @@ __device__ __forceinline__ void dkv_tile(const BwdMaps& m, const BwdParams& p, u
             }
         };
         const float inv = 1.f / p.scale_log2;
-        int2 e = iters > 0 ? tile(t) : make_int2(0, 0);
+        int2 e = JOINED ? e0 : iters > 0 ? tile(t) : make_int2(0, 0);
         if (iters > 0) fetch(e, x);
         for (int it = 0; it < iters; ++it) {
             const int s = it % kStages, row = x * p.N + e.x, valid = JOINED ? e.y & 255 : e.y;
@@ -849,8 +853,7 @@ __device__ __forceinline__ void dkv_tile(const BwdMaps& m, const BwdParams& p, u
         // joined: the lanes that the last tile's and this tile's sums leave alone
         const Lanes lanes(split);
         uint32_t off_last[4] = {}, off[4] = {};
-        int t = 0, cls = 0;
-        if (JOINED && iters > 0) cls = tile(t).y >> 8;
+        int t = 0, cls = e0.y >> 8;
         auto issue_dK = [&](int it, const uint32_t (&skip)[4]) {
             if (!wait(kDS, it)) return false;
             mma_sums<D, JOINED>(c.tmem + kTDK, c.tmem + kTDS, q(it), skip, it > 0, go);
@@ -1016,8 +1019,9 @@ __device__ __forceinline__ void dq_tile(const BwdMaps& m, const BwdParams& p, un
         t += first;
         return p.kcnt ? list[t] : make_int2(t * kTile, min(kTile, p.N - t * kTile));
     };
+    const int2 e0 = JOINED && nt > 0 ? tile(0) : make_int2(0, 0);
     const Cta c = cta_setup<D>(
-        smem_raw, kOffBar, kBars, [](int i) { return i >= kSread ? W::kArrivals : 1; },
+        smem_raw, kOffBar, kBars, p.status, [](int i) { return i >= kSread ? W::kArrivals : 1; },
         [&](const Cta& c) {
             tc::mbar_arrive_expect_tx(c.bar(kQO), 2 * (D / 64) * kRegion);
             for (int h = 0; h < D / 64; ++h) {
@@ -1028,9 +1032,13 @@ __device__ __forceinline__ void dq_tile(const BwdMaps& m, const BwdParams& p, un
 
     if (c.warp == W::kTma) {
         int nland = 0, nk = 0, nv = 0;
+        int2 next = e0;
         for (int t = 0; t < nt; ++t) {
-            int2 e = tile(t);
-            if (JOINED) e.y &= 255;
+            int2 e = JOINED ? next : tile(t);
+            if (JOINED) {
+                e.y &= 255;
+                if (t + 1 < nt) next = tile(t + 1);
+            }
             const int sk = t % kKStages, sv = t % kVStages, row = z * p.N + e.x;
             if (t >= kKStages && !__all_sync(kFull, tc::mbar_wait(c.bar(kKe + sk), (t / kKStages - 1) & 1, c.abort_flag))) break;
             if (!load_tile_zeroed<D>(c, c.base + kOffK + sk * 2 * kRegion, &m.k, kKf + sk, kLand, nland, row, e.y)) break;
@@ -1067,7 +1075,7 @@ __device__ __forceinline__ void dq_tile(const BwdMaps& m, const BwdParams& p, un
         };
         const Lanes lanes(split);
         uint32_t off[4] = {};
-        int cls = JOINED && nt > 0 ? tile(0).y >> 8 : 0;
+        int cls = e0.y >> 8;
         bool ok = nt > 0 && wait(kQO, 0) && issue_S(0) && issue_dP(0);
         for (int t = 0; ok && t < nt; ++t) {
             if (JOINED) {
@@ -1095,7 +1103,7 @@ __device__ __forceinline__ void dq_tile(const BwdMaps& m, const BwdParams& p, un
         const uint64_t cc = pk2(p.scale_log2, p.scale_log2), nl2 = pk2(nl, nl), nd2 = pk2(nd, nd);
         bool ok = true;
         if (JOINED && w < 2) zero_cols<D / 2>(c.tmem + kTDQ + D / 2 * w + lane_off);
-        int valid_next = nt > 0 ? tile(0).y : 0;
+        int valid_next = JOINED ? e0.y : nt > 0 ? tile(0).y : 0;
         for (int t = 0; t < nt; ++t) {
             const int valid = JOINED ? valid_next & 255 : valid_next;
             if (t + 1 < nt) valid_next = tile(t + 1).y;
@@ -1170,8 +1178,6 @@ constexpr int kSmemBytes = kv::Layout<D>::kSmem > dq::kSmem ? kv::Layout<D>::kSm
 template <int D, bool PARTS, bool JOINED>
 __global__ void __launch_bounds__(Warps<D>::kThreads, 1) bwd_kernel(const __grid_constant__ BwdMaps m, const __grid_constant__ BwdParams p) {
     extern __shared__ unsigned char smem_raw[];
-    // a CTA that timed out earlier in this launch (or call) makes the rest return at once
-    if (*reinterpret_cast<volatile int*>(p.status) == kDevTimeout) return;
     const int b = blockIdx.x, early = b - p.kv_first;
     if (early < 0 || (early >= p.q_early && b < p.kv_blocks + p.q_early)) {
         const int i = early < 0 ? b : b - p.q_early, t = PARTS ? i / p.kv_parts : i;
