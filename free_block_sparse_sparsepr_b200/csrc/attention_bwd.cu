@@ -97,7 +97,7 @@ __device__ __forceinline__ void row_terms(const uint4* __restrict__ O, const uin
 // each entry with the groups that keep it (1 the first, 2 the second, 3 both; two more warps per group), and
 // the sums skip the other group's lanes. Which tiles to join depends on how much the lists share: the cut is
 // chosen per KV head and side with the lists at hand (joined_tiles). 24 heads x 8192 tokens, 64 uneven groups,
-// 22% kept: the owned tiles are filled to 1.0 in place of 0.67, 690 us in place of 930; 12 x 16384 1182 and 1370.
+// 22% kept: the owned tiles are filled to 1.0 in place of 0.67, 660 us in place of 930; 12 x 16384 1174 and 1370.
 constexpr int kMaxGroups = 1024;            // of a side
 struct ListParams {
     const int32_t *rowptr, *kg, *qoff, *koff;
