@@ -369,6 +369,10 @@ class SparsePR:
 
     def dense_attn(self, Q, K, V, O=None, stream=None, lse=None):
         """Dense attention; with `lse` (fp32 [B, Hq, N]) the rows' log softmax denominators are written too."""
+        if lse is not None:
+            import torch
+
+            _want("lse", lse, (self.cfg.B, self.cfg.Hq, self.cfg.N), torch.float32, self.device)
         if O is None:
             import torch
 

@@ -1,0 +1,50 @@
+"""What the Python entry points refuse before anything reaches the library: handles without a GPU, on a library
+that only counts its calls."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import free_block_sparse_sparsepr_b200 as spr  # noqa: E402
+
+
+class CountingLibrary:
+    """Every entry point returns success and notes its name."""
+
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.calls.append(name)
+            return 0
+
+        return call
+
+
+def _handle(B=1, Hq=4, Hkv=2, N=32, d=64):
+    h = object.__new__(spr.SparsePR)
+    h.lib, h.h, h.device = CountingLibrary(), 1, torch.device("cpu")
+    h.cfg = spr.Config(B, Hq, Hkv, N, d)
+    return h
+
+
+def _qkv(B=1, Hq=4, Hkv=2, N=32, d=64):
+    return [torch.zeros((B, n, N, d), dtype=torch.bfloat16) for n in (Hq, Hkv, Hkv)]
+
+
+@pytest.mark.parametrize("lse", [torch.zeros((1, 4, 31)), torch.zeros((1, 2, 32)), torch.zeros((1, 4, 32), dtype=torch.bfloat16),
+                                 torch.zeros((1, 4, 32), dtype=torch.float64), torch.zeros((4, 32)), torch.zeros((1, 4, 64))[..., ::2],
+                                 torch.zeros((1, 32, 4)).transpose(1, 2), torch.zeros((1, 4, 32), device="meta")],
+                         ids=lambda t: f"{tuple(t.shape)} {t.dtype} {t.stride()} {t.device}")
+def test_dense_attn_refuses_an_lse_that_the_kernel_would_overrun(lse):
+    h = _handle()
+    with pytest.raises(ValueError, match="lse"):
+        h.dense_attn(*_qkv(), stream=0, lse=lse)
+    assert not h.lib.calls
+
+
+def test_dense_attn_takes_the_lse_that_it_writes():
+    h = _handle()
+    h.dense_attn(*_qkv(), stream=0, lse=torch.zeros((1, 4, 32)))
+    h.dense_attn(*_qkv(), stream=0)
+    assert h.lib.calls == ["sparsepr_dense_attn_lse"] * 2
