@@ -431,6 +431,16 @@ __device__ __forceinline__ Cta cta_setup(unsigned char* smem_raw, int off_bar, i
     return c;
 }
 
+// Whether every MMA has completed (barrier `done`) and no wait of the CTA gave up, for a converged warp whose own
+// waits went `ok`. The flag is read after the barrier: a warp that leaves its loop early, the one that issues the
+// MMAs too, raises it before it arrives there, and a CTA that found the timeout of an earlier one has it up from
+// the start, though each of its waits may succeed at once. Without it such a CTA would store sums that lack a product.
+__device__ __forceinline__ bool sums_complete(const Cta& c, bool ok, int done) {
+    ok = ok && tc::mbar_wait(c.bar(done), 0, c.abort_flag) && !*c.abort_flag;
+    tc::fence_after_sync();
+    return __all_sync(kFull, ok);
+}
+
 // Releases TMEM and reports a wait that gave up; every thread of the CTA calls it last.
 __device__ __forceinline__ void cta_finish(const Cta& c, int* status) {
     tc::fence_before_sync();
@@ -899,7 +909,8 @@ __device__ __forceinline__ void dkv_tile(const BwdMaps& m, const BwdParams& p, u
 #pragma unroll
             for (int i = 0; i < 4; ++i) off_last[i] = off[i];
         }
-        // every issued MMA completes before the sums are read and TMEM is released
+        // every issued MMA completes before the sums are read and TMEM is released; a raised abort flag is seen first
+        __threadfence_block();
         tc::commit_go(c.bar(kDone), go);
         int never = 0;
         tc::mbar_wait(c.bar(kDone), 0, &never);
@@ -970,8 +981,7 @@ __device__ __forceinline__ void dkv_tile(const BwdMaps& m, const BwdParams& p, u
             tc::fence_before_sync();
             tc::mbar_arrive(c.bar(kDS));
         }
-        if (__all_sync(kFull, ok && tc::mbar_wait(c.bar(kDone), 0, c.abort_flag))) {
-            tc::fence_after_sync();
+        if (sums_complete(c, ok, kDone)) {
             const uint32_t acc = c.tmem + (is_dk ? kTDK : kTDV) + col + lane_off;
             // the streamed tiles have all been used: their buffers take the rows
             unsigned char* stage = c.sbase + kOffBuf + c.warp * (32 * kN * 4);
@@ -1088,6 +1098,7 @@ __device__ __forceinline__ void dq_tile(const BwdMaps& m, const BwdParams& p, un
             tc::commit_go(c.bar(kKe + t % kKStages), go);
             tc::commit_go(c.bar(kDSfree), go);
         }
+        __threadfence_block();
         tc::commit_go(c.bar(kDone), go);
         int never = 0;
         tc::mbar_wait(c.bar(kDone), 0, &never);
@@ -1152,8 +1163,7 @@ __device__ __forceinline__ void dq_tile(const BwdMaps& m, const BwdParams& p, un
         }
         // the first two warpgroups store half of the row's columns each
         constexpr int kN = D / 2;
-        if (w < 2 && __all_sync(kFull, ok && tc::mbar_wait(c.bar(kDone), 0, c.abort_flag))) {
-            tc::fence_after_sync();
+        if (w < 2 && sums_complete(c, ok, kDone)) {
             const uint32_t acc = c.tmem + kTDQ + w * kN + lane_off;
             unsigned char* stage = c.sbase + kOffK + c.warp * (32 * kN * 4);     // as in the other pass
             static_assert(8 * 32 * kN * 4 <= (kKStages + kVStages) * 2 * kRegion, "staging");
