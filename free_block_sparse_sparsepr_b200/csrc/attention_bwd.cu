@@ -1198,9 +1198,11 @@ __global__ void __launch_bounds__(Warps<D>::kThreads, 1) bwd_kernel(const __grid
     }
 }
 
-// Sums of the parts in their order, scaled, rounded and written to the output rows: D / 8 threads a row.
+// Sums of the parts in their order, scaled, rounded and written to the output rows: D / 8 threads a row. After a
+// timeout, in this call or one not yet read, sums may be missing and nothing is written.
 template <int D>
 __global__ void __launch_bounds__(256) bwd_join_kernel(const __grid_constant__ BwdParams p) {
+    const int before = *reinterpret_cast<const volatile int*>(p.status);       // looked at last, beside the sums' loads
     const long long t = (long long)blockIdx.x * blockDim.x + threadIdx.x;
     long long row = t / (D / 8);
     const int col = (int)(t % (D / 8)) * 8;
@@ -1223,7 +1225,7 @@ __global__ void __launch_bounds__(256) bwd_join_kernel(const __grid_constant__ B
     const float scale = is_dv ? 1.f : p.scale;
     const long long head = row / p.N, z = q ? head / p.g : head;
     bf16* out = out_row<D>(q ? p.dQ : is_dv ? p.dV : p.dK, q ? p.qperm : p.kperm, head, p.N, (int)(row % p.N), true, z, p.status);
-    if (!out) return;
+    if (!out || before == kDevTimeout) return;
     uint32_t w[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) w[e] = bf16x2(s[2 * e] * scale, s[2 * e + 1] * scale);

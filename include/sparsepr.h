@@ -388,7 +388,8 @@ sparsepr_status sparsepr_dense_attn_lse(sparsepr_handle h, const void* Q, const 
  * the device status word, and the calls can be captured into a graph.
  * SPARSEPR_ERR_WORKSPACE: workspace too small. SPARSEPR_ERR_INVALID_ARG also when the handle's
  * device is not the current one. While the device status word holds SPARSEPR_ERR_TIMEOUT (until
- * sparsepr_device_status reads it) the gradients are left unwritten.
+ * sparsepr_device_status reads it) the gradients are left unwritten; of a call in which a wait runs out
+ * some rows may have been written before, each either whole or not at all.
  */
 sparsepr_status sparsepr_attn_bwd_workspace(sparsepr_handle h, size_t* bytes);
 sparsepr_status sparsepr_dense_attn_bwd(sparsepr_handle h, const void* Q, const void* K, const void* V,

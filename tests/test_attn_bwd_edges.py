@@ -24,7 +24,8 @@ def _workspace(h):
 
 
 @gpu
-@pytest.mark.parametrize("shape,shared", [((4, 40, 40, 100, 128), False), ((4, 76, 38, 100, 64), False)], ids=str)
+@pytest.mark.parametrize("shape,shared", [((1, 1, 1, 640, 128), True), ((1, 3, 1, 300, 64), True),
+                                          ((4, 40, 40, 100, 128), False), ((4, 76, 38, 100, 64), False)], ids=str)
 def test_dense_gradients_stay_unwritten_while_a_timeout_stands(shape, shared):
     """`shared`: CTAs share a tile's stream, so that a kernel of its own joins their sums."""
     _need_gpu()
@@ -49,9 +50,10 @@ def test_dense_gradients_stay_unwritten_while_a_timeout_stands(shape, shared):
 
 @gpu
 @pytest.mark.parametrize("density", [0.0, 0.5])
-@pytest.mark.parametrize("shape,G,launches", [((2, 40, 40, 260, 128), 20, 2), ((4, 40, 20, 400, 64), 4, 3)], ids=str)
+@pytest.mark.parametrize("shape,G,launches", [((1, 1, 1, 2600, 64), 20, 3), ((1, 8, 1, 700, 128), 12, 3),
+                                              ((2, 40, 40, 260, 128), 20, 2), ((4, 40, 20, 400, 64), 4, 3)], ids=str)
 def test_blocksparse_gradients_stay_unwritten_while_a_timeout_stands(shape, G, launches, density):
-    """A tile a group and tiles of two groups; with nothing kept a CTA has nothing to wait for."""
+    """Joined sums, a tile a group and tiles of two groups; with nothing kept a CTA has nothing to wait for."""
     _need_gpu()
     B, Hq, Hkv, N, d = shape
     Q, K, V, dO = _inputs(12, *shape)
