@@ -47,6 +47,7 @@ struct BwdParams {
     int kv_tiles, q_tiles;                  // most key tiles of a KV head, query tiles of a query head
     int kv_parts, q_parts;                  // CTAs that share a tile's stream
     float *kv_part, *q_part;                // their fp32 sums: [part][dV, dK][P N][D], [part][P g N][D]
+    const int32_t* loose;                   // [P][query groups, key groups]: whether their offsets leave rows out (null: dense)
     int kv_blocks;                          // CTAs of dK and dV
     int kv_first, q_early;                  // launch order: so many of dK and dV, so many of dQ, then the others of each
     float scale, scale_log2;
@@ -104,6 +105,7 @@ struct ListParams {
     int2 *klist, *qlist;
     int32_t *kcnt, *qcnt;
     int4 *qtile, *ktile;
+    int32_t* loose;
     int* status;
     int kcap, qcap, q_tiles, kv_tiles, P, N, Gq, Gk, g, joined;
 };
@@ -181,7 +183,11 @@ __device__ void tile_lists(const ListParams& l, int wid, int lane) {
             before += __shfl_sync(kFull, sum, 31);
         }
         for (int t = before + lane; t < cap; t += 32) out[t] = make_int4(0, 0, 0, 0);
-        if (__any_sync(kFull, bad) && lane == 0) set_status(status, kDevBounds);
+        bad = __any_sync(kFull, bad);
+        if (lane == 0) {
+            l.loose[i] = bad;
+            if (bad) set_status(status, kDevBounds);
+        }
         return;
     }
     if (wid >= lists * (l.joined ? 2 : 1)) return;
@@ -1211,7 +1217,11 @@ __global__ void __launch_bounds__(256) bwd_join_kernel(const __grid_constant__ B
     if (q) row -= kv;
     if (q && (p.q_parts <= 1 || !p.dQ || row >= p.qrows)) return;
     const int parts = q ? p.q_parts : p.kv_parts;
-    const long long step = (q ? p.qrows : 2 * p.krows) * D;
+    const bool is_dv = !q && row < p.krows;
+    const long long step = (q ? p.qrows : 2 * p.krows) * D, own = q || is_dv ? row : row - p.krows;
+    const long long head = own / p.N, z = q ? head / p.g : head;
+    const int pos = (int)(own % p.N);
+    const bool loose = p.loose && p.loose[2 * z + !q];
     const float* src = (q ? p.q_part : p.kv_part) + row * D + col;
     float s[8] = {};
     for (int i = 0; i < parts; ++i, src += step) {
@@ -1220,11 +1230,14 @@ __global__ void __launch_bounds__(256) bwd_join_kernel(const __grid_constant__ B
 #pragma unroll
         for (int e = 0; e < 8; ++e) s[e] += v[e];
     }
-    const bool is_dv = !q && row < p.krows;
-    if (!q && !is_dv) row -= p.krows;
     const float scale = is_dv ? 1.f : p.scale;
-    const long long head = row / p.N, z = q ? head / p.g : head;
-    bf16* out = out_row<D>(q ? p.dQ : is_dv ? p.dV : p.dK, q ? p.qperm : p.kperm, head, p.N, (int)(row % p.N), true, z, p.status);
+    if (loose) {        // only rows that a tile holds have sums (bad offsets alone come here)
+        const int4* tile = q ? p.qtile + z * p.q_tiles : p.ktile + z * p.kv_tiles;
+        bool held = false;
+        for (int i = 0; i < (q ? p.q_tiles : p.kv_tiles); ++i) held |= pos >= tile[i].y && pos < tile[i].y + tile[i].z;
+        if (!held) return;
+    }
+    bf16* out = out_row<D>(q ? p.dQ : is_dv ? p.dV : p.dK, q ? p.qperm : p.kperm, head, p.N, pos, true, z, p.status);
     if (!out || before == kDevTimeout) return;
     uint32_t w[4];
 #pragma unroll
@@ -1236,7 +1249,7 @@ size_t align256(size_t b) { return (b + 255) / 256 * 256; }
 
 // Byte offsets of the workspace's parts.
 struct BwdLayout {
-    size_t nlse2, nD, kv_part, q_part, klist, qlist, kcnt, qcnt, qtile, ktile, bytes;
+    size_t nlse2, nD, kv_part, q_part, klist, qlist, kcnt, qcnt, qtile, ktile, loose, bytes;
     int kcap, qcap;
 };
 
@@ -1265,6 +1278,7 @@ BwdLayout bwd_layout(int P, int g, int N, int d, int Gq, int Gk, const BwdParts&
         l.qcnt = take(lists * Gk * sizeof(int32_t));
         l.qtile = take((size_t)P * l.qcap * sizeof(int4));
         l.ktile = take((size_t)P * l.kcap * sizeof(int4));
+        l.loose = take((size_t)P * 2 * sizeof(int32_t));
     }
     l.bytes = at + 240;      // the parts start on 256 bytes, the workspace on 16
     return l;
@@ -1300,6 +1314,7 @@ cudaError_t launch_bwd(const AttnBwdArgs& a, cudaStream_t s) {
         lp.kcnt = reinterpret_cast<int32_t*>(ws + l.kcnt); lp.qcnt = reinterpret_cast<int32_t*>(ws + l.qcnt);
         lp.qtile = reinterpret_cast<int4*>(ws + l.qtile);
         lp.ktile = reinterpret_cast<int4*>(ws + l.ktile);
+        lp.loose = reinterpret_cast<int32_t*>(ws + l.loose);
         lp.q_tiles = p.q_tiles; lp.kv_tiles = p.kv_tiles;
         lp.status = a.status;
         lp.kcap = l.kcap; lp.qcap = l.qcap; lp.P = a.P; lp.N = a.N; lp.Gq = a.Gq; lp.Gk = a.Gk;
@@ -1315,6 +1330,7 @@ cudaError_t launch_bwd(const AttnBwdArgs& a, cudaStream_t s) {
         p.qperm = a.qperm; p.kperm = a.kperm;
         p.klist = lp.klist; p.qlist = lp.qlist; p.kcnt = lp.kcnt; p.qcnt = lp.qcnt;
         p.qtile = lp.qtile; p.ktile = lp.ktile;
+        p.loose = lp.loose;
         p.kcap = l.kcap; p.qcap = l.qcap;
         p.Gq = a.parts.joined ? 2 * a.Gq : a.Gq; p.Gk = a.parts.joined ? 2 * a.Gk : a.Gk;
     }

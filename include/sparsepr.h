@@ -379,7 +379,8 @@ sparsepr_status sparsepr_dense_attn_lse(sparsepr_handle h, const void* Q, const 
  * keys (lse = -inf) has dQ = 0 and adds nothing; a key that no query group keeps has dK = dV = 0.
  * Only kperm, koff, qperm and qoff of `part` and rowptr and kg of `route` are read. Ids, offsets
  * and permutation entries out of range, ids out of order and offsets that leave rows out are
- * skipped and reported as SPARSEPR_ERR_DEVICE in the device status word.
+ * skipped and reported as SPARSEPR_ERR_DEVICE in the device status word; gradient rows that no group or no
+ * permutation entry names then stay unwritten.
  *
  * dQ may be NULL, or dK and dV both, to leave those gradients out. No output may overlap an input
  * or another output. workspace: caller-owned device memory, 16-byte aligned, of at least

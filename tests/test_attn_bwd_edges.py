@@ -74,3 +74,44 @@ def test_blocksparse_gradients_stay_unwritten_while_a_timeout_stands(shape, G, l
         torch.cuda.synchronize()
         assert h.device_status() == 0
     check_gradients(got, _to_original(backward_reference(Q, K, V, O, lse, dO, masks), t, Hq // Hkv), f"after a timeout {shape}")
+
+
+@gpu
+@pytest.mark.parametrize("shape,G", [((1, 1, 1, 2600, 64), 20), ((1, 8, 1, 700, 128), 12), ((2, 40, 40, 260, 128), 20),
+                                     ((4, 40, 20, 400, 64), 4)], ids=str)
+def test_rows_that_no_group_holds_stay_unwritten(shape, G):
+    """Bad offsets are reported, and the rows that they leave out keep what they held."""
+    _need_gpu()
+    B, Hq, Hkv, N, d = shape
+    P, r = B * Hkv, Hq // Hkv
+    Q, K, V, dO = _inputs(13, *shape)
+    t, masks = _routed(13, P, N, G, G, 1.0)
+    even = torch.arange(G + 1, dtype=torch.int32, device="cuda") * N // G
+    t["qoff"], t["koff"] = even.to(torch.int32).repeat(P, 1), even.to(torch.int32).repeat(P, 1)
+    cuts = even.tolist()
+    t["qperm"] = t["kperm"] = torch.arange(N, dtype=torch.int32, device="cuda").repeat(P, 1)
+    O, lse = forward_reference(Q, K, V)
+    args = (O.bfloat16(), lse.float(), dO)
+    z = P - 1
+    with _handle(B, Hq, Hkv, N, d, G, G) as h:
+        ws = _workspace(h)
+        good = h.blocksparse_attn_bwd(Q, K, V, *_structs(t), *args, workspace=ws)
+        torch.cuda.synchronize()
+        assert h.device_status() == 0 and all(torch.isfinite(x).all() for x in good)
+        for side in ("qoff", "koff"):
+            # the first rows; the last; a group whose end lies past N, and with it the next; one that starts before 0
+            for at, value, lost in ((0, 3, (0, 3)), (G, N - 2, (N - 2, N)), (1, N + 5, (0, cuts[2])), (1, -1, (0, cuts[2]))):
+                bad = {k: v.clone() for k, v in t.items()}
+                bad[side][z, at] = value
+                out = _filled(Q, K, V)
+                h.blocksparse_attn_bwd(Q, K, V, *_structs(bad), *args, *out, workspace=ws)
+                torch.cuda.synchronize()
+                assert h.device_status() == 6, (side, at)
+                touched = out[:1] if side == "qoff" else out[1:]
+                for x in touched:
+                    own = x.reshape(P, -1, N, d)[z]
+                    held = torch.ones(N, dtype=torch.bool, device="cuda")
+                    held[lost[0]:lost[1]] = False
+                    assert (own[:, ~held] == 7).all(), (side, at)
+                    assert (own[:, held] != 7).any(-1).all(), (side, at)
+                    assert (x.reshape(P, -1, N, d)[:z] != 7).any(-1).all(), (side, at)
