@@ -502,21 +502,24 @@ __device__ __forceinline__ void mma_sums(uint32_t d_tmem, uint32_t a_tmem, uint3
     }
 }
 
-// D[tmem] += A B^T over one K step of 16: [128][16] tiles without swizzle, as two halves of 8 columns.
-constexpr int kExtBytes = 2 * kTile * 16;
-__device__ __forceinline__ void mma_ext(uint32_t d_tmem, uint32_t a, uint32_t b, uint32_t go) {
+// D[tmem] += A B^T over one K step of 16: [128][8] blocks without swizzle, each with the same block of zeros, which
+// lies behind both, as the other 8 columns.
+constexpr int kExtBlock = kTile * 16;
+__device__ __forceinline__ void mma_ext(uint32_t d_tmem, uint32_t a, uint32_t b, uint32_t zeros, uint32_t go) {
     constexpr uint32_t id = tc::idesc_bf16_f32(kTile, kTile, 0);
-    tc::mma_f16_ss_go(d_tmem, tc::smem_desc_none(a, kTile * 16, 128), tc::smem_desc_none(b, kTile * 16, 128), id, 1u, go);
+    tc::mma_f16_ss_go(d_tmem, tc::smem_desc_none(a, zeros - a, 128), tc::smem_desc_none(b, zeros - b, 128), id, 1u, go);
 }
 
-// x as three bf16 parts that sum to it within 24 bits.
-__device__ __forceinline__ void split3(float x, uint16_t (&o)[3]) {
+// x as three bf16 parts that sum to it within 24 bits, in the first of 8 columns; the others are zero.
+__device__ __forceinline__ uint4 split3(float x) {
+    uint32_t o[3];
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
         const bf16 h = __float2bfloat16_rn(x);
         o[i] = __bfloat16_as_ushort(h);
         x -= bf16_to_f32(h);
     }
+    return make_uint4(o[0] | o[1] << 16, o[2], 0, 0);
 }
 
 template <int D>
@@ -721,7 +724,8 @@ __device__ __forceinline__ bool find_tile(const int4* table, int z, int tiles, i
 // dK(i-1), S(i+1), dV(i): dP and dK run beside the exponentials, S and dV beside dS.
 // The terms -lse and -D of a query vary along the columns here, so a thread would need every query's:
 // they are added by the products instead. One more K step of 16 multiplies ones on the key side with
-// the three bf16 parts (24 bits) of -lse sqrt(d), or of -D, on the query side.
+// the three bf16 parts (24 bits) of -lse sqrt(d), or of -D, on the query side. Each has a block of its own: in
+// one, zeros would have to keep the other's parts out of the product, and zero times NaN is NaN.
 // At d = 64 S and dP have columns of their own: S(i+1) follows the reading of S(i), dP(i+1) that of dP(i).
 // At d = 128 four 128-row buffers hold the streamed tiles. dO(i) is done with a product before Q(i), and Q(i+2)
 // is wanted before dO(i+2): Q(i+2) takes the buffer of dO(i), dO(i+2) that of Q(i).
@@ -734,7 +738,9 @@ constexpr uint32_t kTS = 0;
 template <int D>
 struct Layout {
     static constexpr int kStages = D == 64 ? 4 : 2;
-    static constexpr int kOffExt = kOffBuf + 8 * kRegion, kOffOne = kOffExt + kStages * kExtBytes, kOffBar = kOffOne + 2 * kExtBytes;
+    // parts of -lse and of -D of each stage, the ones, the zeros
+    static constexpr int kOffExt = kOffBuf + 8 * kRegion, kOffOne = kOffExt + kStages * 2 * kExtBlock, kOffZero = kOffOne + kExtBlock,
+                         kOffBar = kOffZero + kExtBlock;
     // full / empty stages (Q's full one also stands for the row terms); S and dP ready, read; P and dS written;
     // all MMAs done; ragged loads
     enum { kOf = kQf + kStages, kQe = kOf + kStages, kOe = kQe + kStages, kS = kOe + kStages, kDP, kDone, kLand, kSread, kDPread,
@@ -759,7 +765,7 @@ __device__ __forceinline__ void dkv_tile(const BwdMaps& m, const BwdParams& p, u
     using W = Warps<D>;
     using L = Layout<D>;
     constexpr int kStages = L::kStages, kTP = L::kTP, kTDS = L::kTDS, kTDV = L::kTDV, kTDK = L::kTDK;
-    constexpr int kOffExt = L::kOffExt, kOffOne = L::kOffOne, kOffBar = L::kOffBar;
+    constexpr int kOffExt = L::kOffExt, kOffOne = L::kOffOne, kOffZero = L::kOffZero, kOffBar = L::kOffBar;
     constexpr int kOf = L::kOf, kQe = L::kQe, kOe = L::kOe, kS = L::kS, kDP = L::kDP, kDone = L::kDone, kLand = L::kLand, kSread = L::kSread,
                   kDPread = L::kDPread, kP = L::kP, kDS = L::kDS, kBars = L::kBars;
     int grp, klo, kn, split, count;
@@ -774,18 +780,12 @@ __device__ __forceinline__ void dkv_tile(const BwdMaps& m, const BwdParams& p, u
     const int t0 = PARTS && nt ? first % nt : 0;
     const int2 e0 = JOINED && iters > 0 ? tile(t0) : make_int2(0, 0);      // read while the CTA sets up
     {
-        // ones under the parts of -lse (columns 0-2), or under those of -D (3-5); the halves of columns
-        // 8-15 are zero everywhere
+        // ones under the parts (columns 0-2), and the zeros
         const uint32_t off = ((tc::smem_addr(smem_raw) + 1023u) & ~1023u) - tc::smem_addr(smem_raw);
-        uint4* ext = reinterpret_cast<uint4*>(smem_raw + off + kOffExt);
+        uint4* ext = reinterpret_cast<uint4*>(smem_raw + off + kOffOne);
         constexpr uint32_t one = 0x3f80u;
-        for (int i = threadIdx.x; i < (kStages + 2) * 2 * kTile; i += W::kThreads) {
-            const int t = i / (2 * kTile);
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (i % (2 * kTile) < kTile && t == kStages) v = make_uint4(one | one << 16, one, 0, 0);
-            if (i % (2 * kTile) < kTile && t == kStages + 1) v = make_uint4(0, one << 16, one | one << 16, 0);
-            ext[i] = v;
-        }
+        for (int i = threadIdx.x; i < 2 * kTile; i += W::kThreads)
+            ext[i] = i < kTile ? make_uint4(one | one << 16, one, 0, 0) : make_uint4(0, 0, 0, 0);
         tc::fence_proxy_async_smem();
     }
     const Cta c = cta_setup<D>(
@@ -825,15 +825,13 @@ __device__ __forceinline__ void dkv_tile(const BwdMaps& m, const BwdParams& p, u
             if (it >= kStages && !__all_sync(kFull, tc::mbar_wait(c.bar((D == 64 ? kQe : kOe) + s), (it / kStages - 1) & 1, c.abort_flag))) break;
             if (!load_tile_zeroed<D>(c, c.base + L::q(it), &m.q, kQf + s, kLand, nland, row, valid)) break;
             nq = it + 1;
-            uint4* ext = reinterpret_cast<uint4*>(c.sbase + kOffExt + s * kExtBytes);
+            uint4* ext = reinterpret_cast<uint4*>(c.sbase + kOffExt + s * 2 * kExtBlock);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                uint16_t a[3], b[3];
-                split3(fmaxf(nl[j] * inv, -1e30f), a);
-                split3(nd[j], b);
-                if (isnan(nl[j])) a[0] = 0x7fffu;       // fmaxf drops NaN
-                ext[32 * j + c.lane] = make_uint4(a[0] | (uint32_t)a[1] << 16, a[2] | (uint32_t)b[0] << 16,
-                                                  b[1] | (uint32_t)b[2] << 16, 0);
+                uint4 a = split3(fmaxf(nl[j] * inv, -1e30f));
+                if (isnan(nl[j])) a.x = 0x7fffu;        // fmaxf drops NaN
+                ext[32 * j + c.lane] = a;
+                ext[kTile + 32 * j + c.lane] = split3(nd[j]);
             }
             tc::fence_proxy_async_smem();
             __syncwarp();
@@ -860,10 +858,10 @@ __device__ __forceinline__ void dkv_tile(const BwdMaps& m, const BwdParams& p, u
         const uint32_t tS = c.tmem + kTS, tDP = c.tmem + L::kTDP;
         auto q = [&](int it) { return c.base + L::q(it); };
         auto o = [&](int it) { return c.base + L::o(it); };
-        auto ext = [&](int it) { return c.base + kOffExt + (it % kStages) * kExtBytes; };
+        auto ext = [&](int it) { return c.base + kOffExt + (it % kStages) * 2 * kExtBlock; };
         auto issue_S = [&](int it) {
             mma_rows<D>(tS, c.base + kOffK, q(it), go);
-            mma_ext(tS, c.base + kOffOne, ext(it), go);
+            mma_ext(tS, c.base + kOffOne, ext(it), c.base + kOffZero, go);
             tc::commit_go(c.bar(kS), go);
         };
         // joined: the lanes that the last tile's and this tile's sums leave alone
@@ -880,7 +878,7 @@ __device__ __forceinline__ void dkv_tile(const BwdMaps& m, const BwdParams& p, u
         if (ok) issue_S(0);
         auto issue_dP = [&](int it) {
             mma_rows<D>(tDP, c.base + kOffV, o(it), go);
-            mma_ext(tDP, c.base + kOffOne + kExtBytes, ext(it), go);
+            mma_ext(tDP, c.base + kOffOne, ext(it) + kExtBlock, c.base + kOffZero, go);
             tc::commit_go(c.bar(kDP), go);
         };
         for (int it = 0; ok && it < iters; ++it) {

@@ -115,3 +115,29 @@ def test_rows_that_no_group_holds_stay_unwritten(shape, G):
                     assert (own[:, ~held] == 7).all(), (side, at)
                     assert (own[:, held] != 7).any(-1).all(), (side, at)
                     assert (x.reshape(P, -1, N, d)[:z] != 7).any(-1).all(), (side, at)
+
+
+@gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+def test_dv_does_not_read_the_output(d, bad):
+    """dV = P^T dO: a row of O that is not finite reaches dQ of its row and dK, never dV."""
+    _need_gpu()
+    for shape in ((1, 2, 1, 200, d), (2, 20, 20, 400, d)):
+        Q, K, V, dO = _inputs(14, *shape)
+        O, lse = forward_reference(Q, K, V)
+        O, lse = O.bfloat16(), lse.float()
+        with _handle(*shape) as h:
+            clean = h.dense_attn_bwd(Q, K, V, O, lse, dO)
+            for i in (0, 63, 127, 128, shape[3] - 1):
+                o = O.clone()
+                o[0, 0, i, 3] = bad
+                dq, dk, dv = h.dense_attn_bwd(Q, K, V, o, lse, dO)
+                assert torch.equal(dv, clean[2]), i
+                assert not torch.isfinite(dq[0, 0, i]).any() and not torch.isfinite(dk[0, 0]).any(), i
+                rest = torch.ones(shape[:2] + shape[3:4], dtype=torch.bool, device="cuda")
+                rest[0, 0, i] = False
+                assert torch.equal(dq[rest], clean[0][rest]), i
+                v = V.clone()
+                v[0, 0, i] = bad
+                assert torch.equal(h.dense_attn_bwd(Q, K, v, O, lse, dO)[2], clean[2]), i
