@@ -591,13 +591,13 @@ __device__ __forceinline__ uint32_t bf16x2(float a, float b) {
 
 // 2^x of a pair on the FMA pipe: x = n + f with n the nearest integer (by adding 1.5 2^23) and |f| <= 1/2,
 // 2^f by a least-maximum polynomial of degree 4 (relative error 2.7e-6, 2^-18.5, fitted here), 2^n from
-// exponent bits. Exponents below -126 give 2^-126; NaN stays NaN (the product keeps it, an addition to the
-// exponent bits would not).
+// exponent bits. Exponents below -126.5 give 0 (n = -127, whose bits are those of 0), as ex2 gives 0 below
+// -126; NaN stays NaN (the product keeps it, an addition to the exponent bits would not).
 __device__ __forceinline__ uint64_t ex2_fma(uint64_t x2) {
     float a, b;
     up2(x2, a, b);
-    asm("max.NaN.f32 %0, %0, 0fC2FC0000;" : "+f"(a));      // -126
-    asm("max.NaN.f32 %0, %0, 0fC2FC0000;" : "+f"(b));
+    asm("max.NaN.f32 %0, %0, 0fC2FE0000;" : "+f"(a));      // -127
+    asm("max.NaN.f32 %0, %0, 0fC2FE0000;" : "+f"(b));
     const uint64_t x = pk2(a, b);
     const uint64_t t = add2(x, pk2(12582912.f, 12582912.f));
     const uint64_t f = fma2(add2(t, pk2(-12582912.f, -12582912.f)), pk2(-1.f, -1.f), x);

@@ -141,3 +141,28 @@ def test_dv_does_not_read_the_output(d, bad):
                 v = V.clone()
                 v[0, 0, i] = bad
                 assert torch.equal(h.dense_attn_bwd(Q, K, v, O, lse, dO)[2], clean[2]), i
+
+
+@gpu
+@pytest.mark.parametrize("shape", [(1, 2, 1, 200, 64), (1, 2, 1, 200, 128), (4, 40, 40, 100, 128)], ids=str)
+def test_rows_left_out_by_their_lse_add_nothing(shape):
+    """lse = -inf: P = 0 in every column, so that not even a dO of 1e34 shows."""
+    _need_gpu()
+    Q, K, V, dO = _inputs(15, *shape)
+    O, lse = forward_reference(Q, K, V)
+    O, lse = O.bfloat16(), lse.float()
+    rows = [0, 5, 64, shape[3] - 1]
+    lse[:, :, rows] = -math.inf
+    O[:, :, rows] = 0
+    big = dO.clone()
+    dO[:, :, rows] = 0
+    big[:, :, rows] = 1e34
+    with _handle(*shape) as h:
+        want = h.dense_attn_bwd(Q, K, V, O, lse, dO)
+        got = h.dense_attn_bwd(Q, K, V, O, lse, big)
+    assert (got[0][:, :, rows] == 0).all()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    kept = torch.ones((shape[3], 1), dtype=torch.bool, device="cuda")
+    kept[rows] = False
+    masks = [kept] * (shape[0] * shape[2])
+    check_gradients(got, backward_reference(Q, K, V, O, lse, dO, masks), f"rows left out {shape}")
