@@ -166,3 +166,89 @@ def test_rows_left_out_by_their_lse_add_nothing(shape):
     kept[rows] = False
     masks = [kept] * (shape[0] * shape[2])
     check_gradients(got, backward_reference(Q, K, V, O, lse, dO, masks), f"rows left out {shape}")
+
+
+def _slopes(Q, K, V, dO, masks, out, step):
+    """Central differences of sum(dO . O) in fp64 along each exact gradient's own direction: its norm, and the
+    direction."""
+    x = [Q.double(), K.double(), V.double()]
+    result = {}
+    for i, name in enumerate(("dQ", "dK", "dV")):
+        u = out[name] / out[name].norm()
+        value = []
+        for s in (step, -step):
+            y = list(x)
+            y[i] = x[i] + s * u
+            value.append((forward_reference(*y, masks)[0] * dO.double()).sum().item())
+        result[name] = ((value[0] - value[1]) / (2 * step), u)
+    return result
+
+
+def _drift(Q, K, O, exact_O, lse, dO, masks):
+    """2-norms of what dQ and dK change by when D = dO.O is taken from a rounded O: P dD k and P dD q, dD = dO.(O - exact)."""
+    B, Hq, N, d = Q.shape
+    r = Hq // K.shape[1]
+    dq, dk = torch.zeros_like(Q, dtype=torch.float64), torch.zeros_like(K, dtype=torch.float64)
+    for b in range(B):
+        for h in range(Hq):
+            z = h // r
+            S = Q[b, h].double() @ K[b, z].double().T / math.sqrt(d) - lse[b, h, :, None]
+            if masks is not None:
+                S = S.masked_fill(~masks[b * K.shape[1] + z], -math.inf)
+            P = S.exp().nan_to_num(0.0) * (dO[b, h].double() * (O[b, h].double() - exact_O[b, h])).sum(1, keepdim=True)
+            dq[b, h] = P @ K[b, z].double() / math.sqrt(d)
+            dk[b, z] += P.T @ Q[b, h].double() / math.sqrt(d)
+    return {"dQ": dq.norm().item(), "dK": dk.norm().item(), "dV": 0.0}
+
+
+def _check_slopes(got, Q, K, V, dO, masks, to_original):
+    """Along u = grad / |grad| the slope is the gradient's norm, so a gradient that is zero, turned around or scaled
+    shows. <got - grad, u> is at most the 2-norm of the error: the kernels' own (backward_reference) and the
+    drift of D. The differences add their own: the third derivative, step^2 / 6 of it (1e-8 of the slope at a
+    step of 1e-4 along a unit vector), and 2^-53 of the value over the step."""
+    exact_O, lse = forward_reference(Q, K, V, masks)
+    O = exact_O.bfloat16()
+    exact = backward_reference(Q, K, V, exact_O, lse, dO, masks)[0]
+    square = backward_reference(Q, K, V, O, lse.float(), dO, masks)[2]
+    drift = _drift(Q, K, O, exact_O, lse, dO, masks)
+    for name, (slope, u) in _slopes(Q, K, V, dO, masks, exact, 1e-4).items():
+        assert abs(slope - exact[name].norm().item()) <= 1e-6 * slope, name       # the formulas against the function
+        slack = square[name].sum().sqrt().item() + drift[name]
+        assert slack <= 0.1 * slope, (name, slack, slope)
+        mine = (got[name].double() * to_original(name, u)).sum().item()
+        assert abs(mine - slope) <= slack + 1e-6 * slope, (name, mine, slope, slack)
+
+
+@gpu
+@pytest.mark.parametrize("shape", [(1, 4, 2, 200, 64), (1, 2, 1, 300, 128)], ids=str)
+def test_differences_along_the_gradients(shape):
+    _need_gpu()
+    B, Hq, Hkv, N, d = shape
+    G = 6
+    Q, K, V, dO = _inputs(3, *shape)
+    with _handle(*shape) as h:
+        O, lse = forward_reference(Q, K, V)
+        got = dict(zip(("dQ", "dK", "dV"), h.dense_attn_bwd(Q, K, V, O.bfloat16(), lse.float(), dO)))
+    _check_slopes(got, Q, K, V, dO, None, lambda n, u: u)
+    t, masks = _routed(3, B * Hkv, N, G, G, 0.5)
+    part, route = _structs(t)
+    with _handle(B, Hq, Hkv, N, d, G, G) as h:
+        O, lse = forward_reference(Q, K, V, masks)
+        got = dict(zip(("dQ", "dK", "dV"), h.blocksparse_attn_bwd(Q, K, V, part, route, O.bfloat16(), lse.float(), dO)))
+    _check_slopes(got, Q, K, V, dO, masks, lambda n, u: _to_original([{n: u}], t, Hq // Hkv)[0][n])
+
+
+def test_the_differences_catch_wrong_gradients():
+    """The check above on the CPU, with the fp64 gradients and with spoiled ones."""
+    g = torch.Generator().manual_seed(3)
+    B, Hq, Hkv, N, d = 1, 2, 1, 40, 16
+    rnd = lambda h: torch.randn((B, h, N, d), generator=g)  # noqa: E731
+    Q, K, V, dO = (x.bfloat16() for x in (rnd(Hq), rnd(Hkv), rnd(Hkv), 0.01 * rnd(Hq)))
+    O, lse = forward_reference(Q, K, V)
+    exact = backward_reference(Q, K, V, O, lse, dO)[0]
+    same = lambda n, u: u  # noqa: E731
+    _check_slopes(exact, Q, K, V, dO, None, same)
+    for name in exact:
+        for spoiled in (torch.zeros_like(exact[name]), -exact[name], 1.2 * exact[name]):
+            with pytest.raises(AssertionError):
+                _check_slopes({**exact, name: spoiled}, Q, K, V, dO, None, same)
