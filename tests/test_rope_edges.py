@@ -1,0 +1,48 @@
+"""Rotary positions: the gradient against the forward map along the turned vector itself."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import free_block_sparse_sparsepr_b200 as spr  # noqa: E402
+from test_rope import CASES, _case, _need_gpu, _reference  # noqa: E402
+
+gpu = pytest.mark.gpu
+
+
+def _check_adjoint(x, y, dx, bound):
+    """<y, R x> = <R^T y, x> for the rounded y that was handed to the gradient: along y itself the left side is
+    |y|^2 up to y's own rounding, so a gradient that is zero, turned around or scaled shows. Allowed, in the
+    2-norm: half a step of y against y, half a step of dx and its bound before that against x."""
+    a, b = (y.double() ** 2).sum().item(), (dx.double() * x.double()).sum().item()
+    eps = lambda t: torch.finfo(t.dtype).eps / 2  # noqa: E731
+    # y = R x (1 + e): |R x - y| is at most half a step of y, and what the bound allows before it
+    slack = ((eps(y) * y.double().norm() + bound.norm()) * y.double().norm()
+             + (eps(dx) * dx.double().norm() + bound.norm()) * x.double().norm()).item()
+    assert slack <= 0.1 * a, (slack, a)
+    assert abs(a - b) <= slack, (a, b, slack)
+
+
+@gpu
+@pytest.mark.parametrize("case", CASES, ids=str)
+def test_gradient_along_the_turned_vector(case):
+    _need_gpu()
+    rope, pos, x, layout = _case(case)
+    y = rope.forward(x, pos)
+    bound = _reference(x, pos, rope, layout, 1.0)[1] * max(1.0, abs(rope.amplitude))
+    _check_adjoint(x, y, rope.backward(y, pos, dtype=x.dtype), bound)
+
+
+def test_the_adjoint_check_catches_wrong_gradients():
+    """The check above on the CPU, with the fp64 map and with spoiled gradients."""
+    rope = spr.Rope(64, (18, 22, 22), layout="half")
+    g = torch.Generator().manual_seed(0)
+    x = torch.randn((1, 50, 3, 64), generator=g).bfloat16()
+    pos = torch.randint(0, 60, (1, 50, 3), generator=g)
+    want, bound = _reference(x, pos, rope, "half", 1.0)
+    y = want.bfloat16()
+    dx = _reference(y, pos, rope, "half", -1.0)[0].bfloat16()
+    _check_adjoint(x, y, dx, bound)
+    turned = _reference(y, pos, rope, "half", 1.0)[0].bfloat16()       # the map itself in place of its transpose
+    for spoiled in (torch.zeros_like(dx), -dx, 1.1 * dx, turned):
+        with pytest.raises(AssertionError):
+            _check_adjoint(x, y, spoiled, bound)
