@@ -530,7 +530,7 @@ class Rope:
             "ntk": base * factor^(w / (w - 2)) in place of base
             "yarn": pairs that turn at least beta_fast times within trained_length keep freq_i, those that
             turn at most beta_slow times take freq_i / factor, a linear ramp over the pair index between;
-            turned pairs are multiplied by 0.1 ln(factor) + 1
+            turned pairs are multiplied by 0.1 ln(factor) + 1 where factor is above 1
     amplitude  factor of the turned pairs; None: the scaling's own"""
 
     def __init__(self, d, widths, layout="half", base=10000.0, scaling="none", factor=1.0, trained_length=None,
@@ -551,7 +551,7 @@ class Rope:
         self.freq = [f for w in widths for f in self._frequencies(w, float(base), scaling, float(factor),
                                                                   trained_length, beta_fast, beta_slow)]
         if amplitude is None:
-            amplitude = 0.1 * math.log(factor) + 1.0 if scaling == "yarn" else 1.0
+            amplitude = 0.1 * math.log(factor) + 1.0 if scaling == "yarn" and factor > 1.0 else 1.0
         self.amplitude = float(amplitude)
         self.lib = load_library()
         self._plans = {}

@@ -46,3 +46,11 @@ def test_the_adjoint_check_catches_wrong_gradients():
     for spoiled in (torch.zeros_like(dx), -dx, 1.1 * dx, turned):
         with pytest.raises(AssertionError):
             _check_adjoint(x, y, spoiled, bound)
+
+
+@pytest.mark.parametrize("factor,amplitude", [(0.25, 1.0), (0.999, 1.0), (1.0, 1.0), (8.0, 1.2079441541679836)])
+def test_a_context_that_is_not_extended_keeps_its_amplitude(factor, amplitude):
+    """yarn: 0.1 ln(factor) + 1 where the context is extended, 1 where the factor is at most 1."""
+    rope = spr.Rope(64, (64,), scaling="yarn", factor=factor, trained_length=4096)
+    assert rope.amplitude == pytest.approx(amplitude, rel=1e-15)
+    assert spr.Rope(64, (64,), scaling="yarn", factor=factor, trained_length=4096, amplitude=1.5).amplitude == 1.5
