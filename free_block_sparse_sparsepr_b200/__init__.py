@@ -233,7 +233,7 @@ class SparsePR:
             import torch
 
             self.device = torch.device("cuda", torch.cuda.current_device())     # the handle's
-        except ImportError:
+        except (ImportError, AssertionError, RuntimeError):      # no torch, or one without CUDA: host buffers only
             self.device = None
 
     @classmethod

@@ -48,3 +48,20 @@ def test_dense_attn_takes_the_lse_that_it_writes():
     h.dense_attn(*_qkv(), stream=0, lse=torch.zeros((1, 4, 32)))
     h.dense_attn(*_qkv(), stream=0)
     assert h.lib.calls == ["sparsepr_dense_attn_lse"] * 2
+
+
+@pytest.mark.parametrize("error", [AssertionError("Torch not compiled with CUDA enabled"), RuntimeError("no CUDA driver")], ids=str)
+def test_a_handle_for_host_buffers_needs_no_cuda_in_torch(monkeypatch, error):
+    lib = CountingLibrary()
+
+    def current_device():
+        raise error
+
+    monkeypatch.setattr(spr, "load_library", lambda: lib)
+    monkeypatch.setattr(torch.cuda, "current_device", current_device)
+    with spr.SparsePR(1, 2, 2, 64, 64, Gk=4, Gq=4) as h:
+        assert lib.calls[0] == "sparsepr_create" and h.device is None
+        with pytest.raises(ValueError, match="Q"):       # no device to hold the gradients' operands against
+            q, k, v = _qkv(1, 2, 2, 64, 64)
+            h.dense_attn_bwd(q, k, v, q, torch.zeros((1, 2, 64)), q)
+    assert "sparsepr_dense_attn_bwd" not in lib.calls
