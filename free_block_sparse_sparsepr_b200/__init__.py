@@ -169,6 +169,8 @@ def _on(device, stream):
 
     if stream is None and device.index == torch.cuda.current_device():
         return _HERE
+    if stream is not None and not isinstance(stream, int) and stream.device != device:
+        raise ValueError(f"stream on {stream.device} for tensors on {device}")
     ctx = contextlib.ExitStack()
     ctx.enter_context(torch.cuda.device(device))
     if stream is not None:

@@ -1,5 +1,7 @@
 """What the Python entry points refuse before anything reaches the library: handles without a GPU, on a library
 that only counts its calls."""
+import types
+
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -65,3 +67,14 @@ def test_a_handle_for_host_buffers_needs_no_cuda_in_torch(monkeypatch, error):
             q, k, v = _qkv(1, 2, 2, 64, 64)
             h.dense_attn_bwd(q, k, v, q, torch.zeros((1, 2, 64)), q)
     assert "sparsepr_dense_attn_bwd" not in lib.calls
+
+
+def test_a_stream_of_another_device_is_refused():
+    """Work on it would reach this device's tensors from the other's context."""
+    h = _handle()
+    q, k, v = _qkv()
+    h._bwd_bytes = 1024
+    other = types.SimpleNamespace(device=torch.device("cuda", 1), cuda_stream=1)
+    with pytest.raises(ValueError, match="stream"):
+        h.dense_attn_bwd(q, k, v, q, torch.zeros((1, 4, 32)), q, stream=other)
+    assert not h.lib.calls
