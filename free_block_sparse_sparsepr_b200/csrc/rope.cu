@@ -265,7 +265,7 @@ sparsepr_status rope(const sparsepr_rope_config* c, const void* src, const int32
     if (c->d != 64 && c->d != 128) return SPARSEPR_ERR_UNSUPPORTED;
     if (c->layout != SPARSEPR_ROPE_INTERLEAVED && c->layout != SPARSEPR_ROPE_HALF) return SPARSEPR_ERR_INVALID_ARG;
     if (c->dtype != SPARSEPR_BF16 && c->dtype != SPARSEPR_FP32) return SPARSEPR_ERR_INVALID_ARG;
-    if (c->axes < 1 || c->axes > 3 || !isfinite(c->amplitude)) return SPARSEPR_ERR_INVALID_ARG;
+    if (c->axes < 1 || c->axes > 3 || !isfinite((float)c->amplitude)) return SPARSEPR_ERR_INVALID_ARG;
     int sum = 0;
     for (int a = 0; a < c->axes; ++a) {
         if (c->width[a] < 2 || c->width[a] % 2 != 0 || c->width[a] > c->d) return SPARSEPR_ERR_INVALID_ARG;
@@ -305,7 +305,10 @@ sparsepr_status rope(const sparsepr_rope_config* c, const void* src, const int32
     }
     const long long model = extent * size;
     const long long head = rows * c->H * c->d * 2;
-    if (overlap(src, bwd ? head : model, dst, bwd ? model : head)) return SPARSEPR_ERR_INVALID_ARG;
+    if (c->B > 1 && c->pos_stride_b > (1ll << 40) / c->B) return SPARSEPR_ERR_UNSUPPORTED;
+    const long long at_bytes = 4 * ((c->B - 1) * c->pos_stride_b + (long long)c->N * c->axes);
+    if (overlap(src, bwd ? head : model, dst, bwd ? model : head) || overlap(pos, at_bytes, dst, bwd ? model : head))
+        return SPARSEPR_ERR_INVALID_ARG;
     RopeParams p;
     memset(&p, 0, sizeof(p));
     int at = 0;

@@ -422,8 +422,8 @@ sparsepr_status sparsepr_blocksparse_attn_bwd(sparsepr_handle h, const void* Qp,
  * sparsepr_rope:     X token-major -> Y bf16 [B][H][N][d]
  * sparsepr_rope_bwd: dY bf16 [B][H][N][d] -> dX token-major, the transposed map; rows of dX must
  *                    not overlap one another
- * pos: int32 [B or 1][N][axes], device. Source and destination must not overlap; both start on 16
- * bytes. Results are rounded once. No handle, no workspace; runs on the current device.
+ * pos: int32 [B or 1][N][axes], device. The destination must not overlap the source or pos; source and
+ * destination start on 16 bytes. Results are rounded once. No handle, no workspace; runs on the current device.
  */
 #define SPARSEPR_ROPE_INTERLEAVED 0
 #define SPARSEPR_ROPE_HALF 1

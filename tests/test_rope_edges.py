@@ -1,10 +1,12 @@
 """Rotary positions: the gradient against the forward map along the turned vector itself."""
+import ctypes
+
 import pytest
 
 torch = pytest.importorskip("torch")
 
 import free_block_sparse_sparsepr_b200 as spr  # noqa: E402
-from test_rope import CASES, _case, _need_gpu, _reference  # noqa: E402
+from test_rope import CASES, _case, _config, _need_gpu, _reference  # noqa: E402
 
 gpu = pytest.mark.gpu
 
@@ -54,3 +56,17 @@ def test_a_context_that_is_not_extended_keeps_its_amplitude(factor, amplitude):
     rope = spr.Rope(64, (64,), scaling="yarn", factor=factor, trained_length=4096)
     assert rope.amplitude == pytest.approx(amplitude, rel=1e-15)
     assert spr.Rope(64, (64,), scaling="yarn", factor=factor, trained_length=4096, amplitude=1.5).amplitude == 1.5
+
+
+def test_positions_inside_the_output_and_huge_amplitudes_are_refused():
+    """The kernel would read positions that it has overwritten, or turn pairs by an infinite fp32 amplitude."""
+    lib = spr.load_library()
+    src, dst = 1 << 20, 1 << 40
+    out = 2 * 4 * 64 * 2                       # bytes of [1, 2, 4, 64] bf16 on either side
+    for fn in (lib.sparsepr_rope, lib.sparsepr_rope_bwd):
+        for pos in (dst, dst + out - 4, dst - 12):
+            assert fn(ctypes.byref(_config()), src, pos, dst, None) == 1
+        # positions of a second sample, as far away as pos_stride_b says
+        c = _config(B=2, stride_b=512, pos_stride_b=100)
+        assert fn(ctypes.byref(c), src, dst - 400, dst, None) == 1
+        assert fn(ctypes.byref(_config(amplitude=1e39)), src, 1 << 30, dst, None) == 1
