@@ -113,6 +113,7 @@ def load_library() -> ctypes.CDLL:
         "sparsepr_dense_attn": (st, [H, _p, _p, _p, _p, _p]),
         "sparsepr_dense_attn_lse": (st, [H, _p, _p, _p, _p, _p, _p]),
         "sparsepr_attn_bwd_workspace": (st, [H, ctypes.POINTER(ctypes.c_size_t)]),
+        "sparsepr_dense_attn_bwd_workspace": (st, [H, ctypes.POINTER(ctypes.c_size_t)]),
         "sparsepr_dense_attn_bwd": (st, [H] + [_p] * 10 + [ctypes.c_size_t, _p]),
         "sparsepr_blocksparse_attn_bwd": (st, [H, _p, _p, _p, ctypes.POINTER(Partition), ctypes.POINTER(Route)]
                                           + [_p] * 7 + [ctypes.c_size_t, _p]),
@@ -230,7 +231,8 @@ class SparsePR:
         h = _p()
         _check("sparsepr_create", self.lib.sparsepr_create(ctypes.byref(self.cfg), ctypes.byref(h)))
         self.h = h
-        self._bwd_bytes = self.attn_bwd_workspace_bytes()
+        self._bwd_bytes = {"sparsepr_dense_attn_bwd": self.attn_bwd_workspace_bytes(dense_only=True),
+                           "sparsepr_blocksparse_attn_bwd": self.attn_bwd_workspace_bytes()}
         try:
             import torch
 
@@ -384,9 +386,11 @@ class SparsePR:
         return O
 
     # ------------------------------------------------------------------ backward passes
-    def attn_bwd_workspace_bytes(self) -> int:
+    def attn_bwd_workspace_bytes(self, dense_only=False) -> int:
+        """Workspace of either backward pass, or what dense_attn_bwd alone needs."""
         n = ctypes.c_size_t()
-        _check("sparsepr_attn_bwd_workspace", self.lib.sparsepr_attn_bwd_workspace(self.h, ctypes.byref(n)))
+        fn = "sparsepr_dense_attn_bwd_workspace" if dense_only else "sparsepr_attn_bwd_workspace"
+        _check(fn, getattr(self.lib, fn)(self.h, ctypes.byref(n)))
         return n.value
 
     def _bwd(self, name, call, Q, K, V, O, lse, dO, dQ, dK, dV, need_dq, need_dkv, workspace, stream):
@@ -418,7 +422,7 @@ class SparsePR:
                 dK = torch.empty_like(K) if dK is None else dK
                 dV = torch.empty_like(V) if dV is None else dV
             if workspace is None:
-                workspace = torch.empty(self._bwd_bytes, dtype=torch.uint8, device=dev)
+                workspace = torch.empty(self._bwd_bytes[name], dtype=torch.uint8, device=dev)
             _check(name, call(Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(), lse.data_ptr(), dO.data_ptr(),
                               _ptr(dQ), _ptr(dK), _ptr(dV), workspace.data_ptr(),
                               workspace.numel() * workspace.element_size(), _stream_on(dev, stream)))
@@ -427,8 +431,8 @@ class SparsePR:
     def dense_attn_bwd(self, Q, K, V, O, lse, dO, dQ=None, dK=None, dV=None, need_dq=True, need_dkv=True,
                        workspace=None, stream=None):
         """Gradients (dQ, dK, dV) of dense_attn from its output O and lse and the gradient dO of O (None for
-        one that need_dq / need_dkv leave out). workspace: attn_bwd_workspace_bytes() of device memory that
-        a program may keep; None takes it from torch for this call."""
+        one that need_dq / need_dkv leave out). workspace: attn_bwd_workspace_bytes(dense_only=True) of device
+        memory that a program may keep; None takes it from torch for this call."""
         return self._bwd("sparsepr_dense_attn_bwd",
                          lambda *a: self.lib.sparsepr_dense_attn_bwd(self.h, *a),
                          Q, K, V, O, lse, dO, dQ, dK, dV, need_dq, need_dkv, workspace, stream)
@@ -437,7 +441,7 @@ class SparsePR:
                              dV=None, need_dq=True, need_dkv=True, workspace=None, stream=None):
         """Gradients of permute followed by blocksparse_attn, with the partition and the route held constant:
         group-major Qp, Kp, Vp, Osp, lse and dOsp in (dOsp: permute of the original-order gradient), dQ, dK
-        and dV in the original token order out. A partition or route whose buffers the handle owns is
+        and dV in the original token order out. workspace: attn_bwd_workspace_bytes(). A partition or route whose buffers the handle owns is
         overwritten by the handle's next call: keep copies (partition_views, route_views) across calls."""
         return self._bwd("sparsepr_blocksparse_attn_bwd",
                          lambda q, k, v, *a: self.lib.sparsepr_blocksparse_attn_bwd(

@@ -1011,6 +1011,12 @@ sparsepr_status sparsepr_attn_bwd_workspace(sparsepr_handle h, size_t* bytes) {
     return SPARSEPR_OK;
 }
 
+sparsepr_status sparsepr_dense_attn_bwd_workspace(sparsepr_handle h, size_t* bytes) {
+    if (!h || !bytes) return SPARSEPR_ERR_INVALID_ARG;
+    *bytes = h->bwd_bytes[0];
+    return SPARSEPR_OK;
+}
+
 sparsepr_status sparsepr_dense_attn_bwd(sparsepr_handle h, const void* Q, const void* K, const void* V, const void* O,
                                         const float* lse, const void* dO, void* dQ, void* dK, void* dV,
                                         void* workspace, size_t workspace_bytes, void* stream) {

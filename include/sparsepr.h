@@ -383,16 +383,20 @@ sparsepr_status sparsepr_dense_attn_lse(sparsepr_handle h, const void* Q, const 
  * permutation entry names then stay unwritten.
  *
  * dQ may be NULL, or dK and dV both, to leave those gradients out. No output may overlap an input
- * or another output. workspace: caller-owned device memory, 16-byte aligned, of at least
- * sparsepr_attn_bwd_workspace bytes (enough for either call), used until the call's work has
- * finished; calls with different workspaces may overlap. Nothing else of the handle is written but
- * the device status word, and the calls can be captured into a graph.
+ * or another output. workspace: caller-owned device memory, 16-byte aligned, used until the call's work has
+ * finished, of at least sparsepr_attn_bwd_workspace bytes (enough for either call) or, for the dense call,
+ * sparsepr_dense_attn_bwd_workspace bytes. The block-sparse call keeps up to two lists for every group of a side,
+ * each with room for N / 128 entries and one a group of the other side, 8 bytes an entry: for 24 heads x
+ * 118800 tokens 257 MB in all with 256 groups a side and 1.56 GB with 1024, where the dense call needs 23 MB.
+ * The calls write nothing of the handle on the device but its status word, so, issued one after another by the
+ * host, the work of calls with different workspaces may overlap there; and they can be captured into a graph.
  * SPARSEPR_ERR_WORKSPACE: workspace too small. SPARSEPR_ERR_INVALID_ARG also when the handle's
  * device is not the current one. While the device status word holds SPARSEPR_ERR_TIMEOUT (until
  * sparsepr_device_status reads it) the gradients are left unwritten; of a call in which a wait runs out
  * some rows may have been written before, each either whole or not at all.
  */
 sparsepr_status sparsepr_attn_bwd_workspace(sparsepr_handle h, size_t* bytes);
+sparsepr_status sparsepr_dense_attn_bwd_workspace(sparsepr_handle h, size_t* bytes);
 sparsepr_status sparsepr_dense_attn_bwd(sparsepr_handle h, const void* Q, const void* K, const void* V,
                                         const void* O, const float* lse, const void* dO, void* dQ, void* dK,
                                         void* dV, void* workspace, size_t workspace_bytes, void* stream);

@@ -1,6 +1,7 @@
 """Backward passes where a call meets what it must leave alone: a timeout that has not been read, rows that bad
 offsets leave out, non-finite values in operands that a gradient does not read, rows left out by lse = -inf; and
 directional differences along the gradients themselves."""
+import ctypes
 import math
 
 import pytest
@@ -252,3 +253,37 @@ def test_the_differences_catch_wrong_gradients():
         for spoiled in (torch.zeros_like(exact[name]), -exact[name], 1.2 * exact[name]):
             with pytest.raises(AssertionError):
                 _check_slopes({**exact, name: spoiled}, Q, K, V, dO, None, same)
+
+
+@gpu
+def test_a_dense_call_needs_no_room_for_lists():
+    _need_gpu()
+    B, Hq, Hkv, N, d, G = 1, 4, 2, 1500, 64, 500
+    Q, K, V, dO = _inputs(16, B, Hq, Hkv, N, d)
+    with _handle(B, Hq, Hkv, N, d, G, G) as h, _handle(B, Hq, Hkv, N, d) as plain:
+        lse = torch.empty((B, Hq, N), device="cuda")
+        O = h.dense_attn(Q, K, V, lse=lse)
+        n, both = h.attn_bwd_workspace_bytes(dense_only=True), h.attn_bwd_workspace_bytes()
+        assert n == plain.attn_bwd_workspace_bytes(dense_only=True) and both > max(n, 2 * Hkv * G * G * 8)
+        ws = torch.full((n + 512,), 0x5A, dtype=torch.uint8, device="cuda")
+        got = h.dense_attn_bwd(Q, K, V, O, lse, dO, workspace=ws[256:256 + n])
+        assert (ws[:256] == 0x5A).all() and (ws[256 + n:] == 0x5A).all()
+        # without one, no more is taken for the call
+        del ws
+        torch.cuda.synchronize()
+        torch.cuda.empty_cache()
+        held = torch.cuda.memory_allocated()
+        torch.cuda.reset_peak_memory_stats()
+        again = h.dense_attn_bwd(Q, K, V, O, lse, dO)
+        own = sum(x.numel() * 2 for x in again)
+        assert torch.cuda.max_memory_allocated() - held <= own + n + 4 * 512
+        assert all(torch.equal(a, b) for a, b in zip(got, again))
+        t, _ = _routed(16, B * Hkv, N, G, G, 0.3)
+        with pytest.raises(spr.SparsePRError) as e:
+            h.blocksparse_attn_bwd(Q, K, V, *_structs(t), O, lse, dO, workspace=torch.empty(n, dtype=torch.uint8, device="cuda"))
+        assert e.value.code == 3
+
+
+def test_null_workspace_queries_without_gpu():
+    n = ctypes.c_size_t()
+    assert spr.load_library().sparsepr_dense_attn_bwd_workspace(None, ctypes.byref(n)) == 1

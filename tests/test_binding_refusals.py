@@ -73,7 +73,6 @@ def test_a_stream_of_another_device_is_refused():
     """Work on it would reach this device's tensors from the other's context."""
     h = _handle()
     q, k, v = _qkv()
-    h._bwd_bytes = 1024
     other = types.SimpleNamespace(device=torch.device("cuda", 1), cuda_stream=1)
     with pytest.raises(ValueError, match="stream"):
         h.dense_attn_bwd(q, k, v, q, torch.zeros((1, 4, 32)), q, stream=other)
