@@ -221,7 +221,10 @@ def device_view(ptr: int, shape, dtype):
 
 
 class SparsePR:
-    """One configured SparsePR call on the current CUDA device (owns the workspace)."""
+    """One configured SparsePR call on the current CUDA device (owns the workspace).
+
+    No call is an autograd function: results carry no graph whatever their inputs require. dense_attn and
+    blocksparse_attn have their gradients in dense_attn_bwd and blocksparse_attn_bwd, the other steps none."""
 
     def __init__(self, B, Hq, Hkv, N, d, Gk, Gq, block=128, rK=48, rQ=64, M=64, r=16, kmeans_iters=10,
                  lam=0.1, rho_exec=0.22, flags=0, seed=0):
@@ -439,7 +442,8 @@ class SparsePR:
 
     def blocksparse_attn_bwd(self, Qp, Kp, Vp, part: Partition, route: Route, Osp, lse, dOsp, dQ=None, dK=None,
                              dV=None, need_dq=True, need_dkv=True, workspace=None, stream=None):
-        """Gradients of permute followed by blocksparse_attn, with the partition and the route held constant:
+        """Gradients of permute followed by blocksparse_attn, with the partition and the route held constant (and of
+        writeback without a fit; the correction of one with a fit, or of `attention`, has no gradient here):
         group-major Qp, Kp, Vp, Osp, lse and dOsp in (dOsp: permute of the original-order gradient), dQ, dK
         and dV in the original token order out. workspace: attn_bwd_workspace_bytes(). A partition or route whose buffers the handle owns is
         overwritten by the handle's next call: keep copies (partition_views, route_views) across calls."""
@@ -526,7 +530,8 @@ class SparsePR:
 
 class Rope:
     """Rotary positions of Q and K: from a model's token-major tensors into the head-major bf16
-    layout of the attention calls (`forward`), and the gradient back (`backward`).
+    layout of the attention calls (`forward`), and the gradient back (`backward`). No autograd function:
+    results carry no graph whatever their inputs require, the gradient is a call of its own.
 
     widths  rotated elements of each axis, even: (w,) for a sequence (w < d rotates part of the head),
             (frame, row, column) for video tokens

@@ -15,9 +15,11 @@
 // 1.7e-3 for an eighth product (4096 rows, 12 heads: 17% more time; 24 x 8192: 12%). lse, D, the logits and all
 // sums are fp32.
 //
-// Bound by the tensor pipe (74% of its cycles at 4096 rows, d = 128) and, in long calls, by the power cap: 12 heads x
-// 4096 rows, d = 128 take 266 us (969 TFLOP/s of 10 N^2 d a head), 24 x 8192 2.21 ms (932 TFLOP/s, the seven
-// products at 1.30 PFLOP/s), 24 x 4096 at d = 64 378 us (682 TFLOP/s).
+// Bound by the tensor pipe (74% of its cycles at 4096 rows, d = 128) and, in long calls, by the power cap; at d = 64,
+// where the products are half as long and the arithmetic is not, by the hand-over between the two (tensor pipe
+// 50%, issue slots 60%). A call among others, the power cap settled: 12 heads x 4096 rows, d = 128 309 us (834
+// TFLOP/s of 10 N^2 d a head), 24 x 8192 2.27 ms (907 TFLOP/s, the seven products at 1.27 PFLOP/s), 24 x 4096 at
+// d = 64 416 us (619 TFLOP/s). Short graph runs, before it settles: 268 to 290 us, 2.21 to 2.25 ms, 380 us.
 #include <math.h>
 #include <string.h>
 
@@ -800,7 +802,8 @@ __device__ __forceinline__ void dkv_tile(const BwdMaps& m, const BwdParams& p, u
 
     if (c.warp == W::kTma) {
         int nland = 0, nq = 0, no = 0, t = t0, x = z * p.g + (PARTS && nt ? first / nt : 0);
-        // this lane's four rows of the next tile's terms; rows past its end give P = 2^(-huge) = 0
+        // this lane's four rows of the next tile's terms; rows past its end give P = 2^(-huge) = 0 (and their
+        // Q and dO are zeroed)
         float nl[4], nd[4];
         auto fetch = [&](int2 e, int head) {
 #pragma unroll
@@ -1369,7 +1372,9 @@ cudaError_t launch_bwd(const AttnBwdArgs& a, cudaStream_t s) {
 // sums takes 2.5 for its launch and 1 per 4 MB written and read back. Few CTAs with long streams gain most, and a number of
 // CTAs just past a multiple of the SMs is stepped over. On the device, whole against shared (d = 128, one
 // sample): 4 query heads on 1 KV head, 1000 tokens 54 against 17 us; 3 on 1, 4096 tokens 142 against 85;
-// 12 heads, 1024 tokens 30 against 45 (left whole).
+// 12 heads, 1024 tokens 30 against 45 (left whole). The times are those of d = 128. At d = 64 a tile takes 0.7 to
+// 0.8 of them, which moves few borders, and the choices hold: 39 against 17 us, 103 against 62, 24 (left whole)
+// against 28; 2 heads, 1300 tokens 17.5 against 15.1; 1 head, 8192 tokens 72 (left whole) against 105.
 struct BwdModel {
     double nk, nq, tk, tq;                  // CTAs of dK and dV, of dQ; their times
     int sms;
@@ -1421,7 +1426,8 @@ BwdParts attn_bwd_parts(int P, int g, int N, int d, int Gq, int Gk, bool sparse,
     best.joined = joined(best);
     // The order, for equal streams: m SMs turn to dQ before their last CTA of dK and dV, m others run one
     // more of those (12 heads, 4096 tokens: 277 -> 271 us with m = 28; 16 on 4 heads, 2 x 2311: 257 -> 252 with
-    // 32). Here the times are those of steady tiles and of whole CTAs, by clock reads in long launches.
+    // 32; at d = 64 208 -> 205 and 192.2 -> 191.0). Here the times are those of steady tiles and of whole CTAs at
+    // d = 128, by clock reads in long launches.
     if (!sparse && best.kv == 1 && best.q == 1) {
         const BwdModel w = {ctas * P, ctas * P * g, 1.35 * len * g + 4.4, 0.98 * len + 3.1, sms};
         const int rest = (int)w.nk % sms, each = (int)ceil(w.tk / w.tq);

@@ -3,9 +3,10 @@
 // dx = amplitude * R(pos)^T dy back. A pair (a, b) turned by the angle pos * freq becomes
 // (a cos - b sin, a sin + b cos); elements past the rotated width pass through unscaled.
 //
-// Angles are formed in turns as 64-bit fixed point: freq / 2 pi is held as a fraction of 2^64, so
-// pos times it, modulo 2^64, is the angle's fraction of a turn with an error below
-// |pos| 2^-53 turns (the fraction comes from a double), for every 32-bit position.
+// Angles are formed in turns as 64-bit fixed point: freq / 2 pi is held as a fraction of 2^64 and
+// pos times it, modulo 2^64, is the angle's fraction of a turn, of which the upper 32 bits are kept. For
+// every 32-bit position the error is below 2^-32 turn (1.5e-9 rad) for that cut, and |pos| 2^-52
+// max(1, |freq| / 2 pi) turns, since the quotient comes from a double division by a rounded 2 pi.
 #include <math.h>
 #include <string.h>
 
@@ -139,7 +140,7 @@ struct Walk {
 // head and walks over the block's heads with the angles in registers. Consecutive threads hold
 // consecutive vectors, so that every store fills whole 32-byte sectors. Bound by HBM: bf16 queries of
 // 32760 tokens x 24 heads take 67 us (6.0 TB/s, 0.92 of the measured copy rate), the fp32 gradient
-// of 75600 tokens x 8 heads 76 us (6.1 TB/s, 0.93).
+// of 75600 tokens x 8 heads 75 us (6.2 TB/s, 0.95), fp32 queries of 32760 x 24 94 us (6.4 TB/s, 0.98).
 template <typename T, int D, bool HALF, bool BWD>
 __global__ void __launch_bounds__(kThreads) rope_vec_kernel(const __grid_constant__ RopeParams p) {
     constexpr int kUnits = D / 16;
@@ -194,7 +195,10 @@ __global__ void __launch_bounds__(kThreads) rope_vec_kernel(const __grid_constan
 }
 
 // Scalar kernel, for half layouts whose sections do not split into vectors: a lane holds pairs
-// `lane` and `lane + 32` of a token's head, consecutive lanes consecutive elements.
+// `lane` and `lane + 32` of a token's head, consecutive lanes consecutive elements. Each load and store moves
+// one element a lane, so that there are eight times as many as the vector kernel needs for bf16 and too
+// few bytes are in flight: sections of 44, 42 and 42, 32760 tokens x 24 heads, bf16 take 121 us (3.3 TB/s, 0.51 of
+// the measured copy rate), their gradient 116 us.
 template <typename T, int D, bool BWD>
 __global__ void __launch_bounds__(kThreads) rope_scalar_kernel(const __grid_constant__ RopeParams p) {
     const int lane = threadIdx.x & 31;
