@@ -27,6 +27,7 @@ FLAG_PROBES_RANDOM = 1 << 6      # ablation: probes drawn at random (seeded Spli
 FLAG_SEMANTIC_PARTITION = 1 << 7  # ablation: k-means on the raw keys and the raw mean query
 FLAG_STAGE_TIMING = 1 << 8
 FLAG_TEST_STALL = 1 << 9          # test only: the dense kernel's first bounded wait runs out
+FLAG_BWD_SPLIT_DS = 1 << 10       # backward passes: dS as two bf16 parts in dQ, at the price of an eighth product
 
 STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported configuration", 3: "workspace allocation failed",
           4: "CUDA error", 5: "device wait timed out", 6: "device-side check failed"}
@@ -674,5 +675,5 @@ def route_from_tensors(t: dict) -> Route:
 __all__ = ["SparsePR", "Rope", "RopeConfig", "SparsePRError", "Config", "Partition", "Route", "Fit", "Stats", "load_library",
            "header_functions", "partition_from_tensors", "route_from_tensors", "device_view", "LIB_PATH",
            "FLAG_HARD_DROP_ONLY", "FLAG_RIDGE_ONLY", "FLAG_RBAR_UNPROJECTED", "FLAG_UNIFORM_WEIGHTS", "FLAG_TOPMASS",
-           "FLAG_PROBES_UNIFORM", "FLAG_PROBES_RANDOM", "FLAG_SEMANTIC_PARTITION", "SHARED_ROWS",
+           "FLAG_PROBES_UNIFORM", "FLAG_PROBES_RANDOM", "FLAG_BWD_SPLIT_DS", "FLAG_SEMANTIC_PARTITION", "SHARED_ROWS",
            "FLAG_STAGE_TIMING"]

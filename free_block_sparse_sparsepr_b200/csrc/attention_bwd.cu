@@ -11,9 +11,10 @@
 // Roundings: P and dS become bf16 (2^-8 of each element at most) because the tensor cores take no fp32
 // operand, and TF32 would halve their rate. In the 2-norm against fp64 that leaves dQ at 2.5 to 3.0e-3, dK and dV at
 // 2.2 to 2.4e-3, where rounding the exact gradients to bf16 costs 1.7e-3. dQ suffers most: sum_j dS_ij = 0 takes
-// the keys' common part out of the gradient but not out of the errors. A second bf16 part of dS brings dQ to
-// 1.7e-3 for an eighth product (4096 rows, 12 heads: 17% more time; 24 x 8192: 12%). lse, D, the logits and all
-// sums are fp32.
+// the keys' common part out of the gradient but not out of the errors. The caller may have dS in two bf16 parts
+// there (SPLIT): dQ is then at 1.66e-3 for an eighth product, 10 to 14% more time a call (12 heads x 4096 rows
+// 314 -> 359 us, 24 x 8192 2.31 -> 2.57 ms, d = 64 24 x 4096 422 -> 470 us; 24 x 8192 at 22% kept 755 -> 829 us).
+// lse, D, the logits and all sums are fp32.
 //
 // Bound by the tensor pipe (74% of its cycles at 4096 rows, d = 128) and, in long calls, by the power cap; at d = 64,
 // where the products are half as long and the arithmetic is not, by the hand-over between the two (tensor pipe
@@ -591,6 +592,11 @@ __device__ __forceinline__ uint32_t bf16x2(float a, float b) {
     return *reinterpret_cast<uint32_t*>(&v);
 }
 
+// What rounding a and b to the bf16 pair `v` left over, rounded in turn.
+__device__ __forceinline__ uint32_t bf16x2_rest(float a, float b, uint32_t v) {
+    return bf16x2(a - __uint_as_float(v << 16), b - __uint_as_float(v & 0xffff0000u));
+}
+
 // 2^x of a pair on the FMA pipe: x = n + f with n the nearest integer (by adding 1.5 2^23) and |f| <= 1/2,
 // 2^f by a least-maximum polynomial of degree 4 (relative error 2.7e-6, 2^-18.5, fitted here), 2^n from
 // exponent bits. Exponents below -126.5 give 0 (n = -127, whose bits are those of 0), as ex2 gives 0 below
@@ -1017,10 +1023,11 @@ enum { kQO = 0, kKf = 1, kVf = kKf + kKStages, kKe = kVf + kVStages, kVe = kKe +
        kDone, kLand, kSread, kDPread, kDS, kBars };
 constexpr int kSmem = kOffBar + 8 * kBars + 16 + 1024;
 static_assert(kSmem <= 232448, "shared memory budget");
-constexpr uint32_t kTS = 0, kTDP = 128, kTDQ = 256, kTDS = 384;
+constexpr uint32_t kTS = 0, kTDP = 128, kTDQ = 256, kTDS = 384, kTDSlow = 448;
 }  // namespace dq
 
-template <int D, bool PARTS, bool JOINED>
+// With SPLIT dS enters dQ as two bf16 parts (16 bits), an eighth product; the second has the last 64 TMEM columns.
+template <int D, bool PARTS, bool JOINED, bool SPLIT>
 __device__ __forceinline__ void dq_tile(const BwdMaps& m, const BwdParams& p, unsigned char* smem_raw, int x, int pair, int part) {
     using namespace dq;
     using W = Warps<D>;
@@ -1102,6 +1109,7 @@ __device__ __forceinline__ void dq_tile(const BwdMaps& m, const BwdParams& p, un
             if (t + 1 < nt && !(wait(kSread, t) && issue_S(t + 1) && wait(kDPread, t) && issue_dP(t + 1))) break;
             if (!wait(kDS, t)) break;
             mma_sums<D, JOINED>(c.tmem + kTDQ, c.tmem + kTDS, k(t), off, t > 0, go);
+            if (SPLIT) mma_sums<D, JOINED>(c.tmem + kTDQ, c.tmem + kTDSlow, k(t), off, true, go);
             tc::commit_go(c.bar(kKe + t % kKStages), go);
             tc::commit_go(c.bar(kDSfree), go);
         }
@@ -1127,7 +1135,7 @@ __device__ __forceinline__ void dq_tile(const BwdMaps& m, const BwdParams& p, un
             if (t + 1 < nt) valid_next = tile(t + 1).y;
             if (!__all_sync(kFull, tc::mbar_wait(c.bar(kS), t & 1, c.abort_flag))) { ok = false; break; }
             tc::fence_after_sync();
-            uint32_t pv[W::kH][32], pk[16 * W::kH];
+            uint32_t pv[W::kH][32], pk[16 * W::kH], low[16 * W::kH];
             load_cols(tS, pv);
             tc::fence_before_sync();
             tc::mbar_arrive(c.bar(kSread));
@@ -1158,12 +1166,15 @@ __device__ __forceinline__ void dq_tile(const BwdMaps& m, const BwdParams& p, un
                              pk2(__uint_as_float(pv[h][2 * e]), __uint_as_float(pv[h][2 * e + 1]))),
                         x0, x1);
                     pk[16 * h + e] = bf16x2(x0, x1);
+                    if (SPLIT) low[16 * h + e] = bf16x2_rest(x0, x1, pk[16 * h + e]);
                 }
             }
             if (t > 0 && !__all_sync(kFull, tc::mbar_wait(c.bar(kDSfree), (t - 1) & 1, c.abort_flag))) { ok = false; break; }
             tc::fence_after_sync();
             if (W::kH == 2) tc::tmem_st32(tDS, pk);
             else tc::tmem_st16(tDS, pk);
+            if (SPLIT && W::kH == 2) tc::tmem_st32(tDS + kTDSlow - kTDS, low);
+            if (SPLIT && W::kH == 1) tc::tmem_st16(tDS + kTDSlow - kTDS, low);
             tc::tmem_wait_st();
             tc::fence_before_sync();
             tc::mbar_arrive(c.bar(kDS));
@@ -1192,7 +1203,7 @@ __device__ __forceinline__ void dq_tile(const BwdMaps& m, const BwdParams& p, un
 template <int D>
 constexpr int kSmemBytes = kv::Layout<D>::kSmem > dq::kSmem ? kv::Layout<D>::kSmem : dq::kSmem;
 
-template <int D, bool PARTS, bool JOINED>
+template <int D, bool PARTS, bool JOINED, bool SPLIT>
 __global__ void __launch_bounds__(Warps<D>::kThreads, 1) bwd_kernel(const __grid_constant__ BwdMaps m, const __grid_constant__ BwdParams p) {
     extern __shared__ unsigned char smem_raw[];
     const int b = blockIdx.x, early = b - p.kv_first;
@@ -1201,7 +1212,7 @@ __global__ void __launch_bounds__(Warps<D>::kThreads, 1) bwd_kernel(const __grid
         dkv_tile<D, PARTS, JOINED>(m, p, smem_raw, t / p.kv_tiles, t % p.kv_tiles, PARTS ? i % p.kv_parts : 0);
     } else {
         const int i = early < p.q_early ? early : b - p.kv_blocks, t = PARTS ? i / p.q_parts : i;
-        dq_tile<D, PARTS, JOINED>(m, p, smem_raw, t / p.q_tiles, t % p.q_tiles, PARTS ? i % p.q_parts : 0);
+        dq_tile<D, PARTS, JOINED, SPLIT>(m, p, smem_raw, t / p.q_tiles, t % p.q_tiles, PARTS ? i % p.q_parts : 0);
     }
 }
 
@@ -1350,8 +1361,11 @@ cudaError_t launch_bwd(const AttnBwdArgs& a, cudaStream_t s) {
     p.kv_first = both ? p.kv_blocks - a.parts.kv_late : p.kv_blocks;
     p.q_early = both ? a.parts.q_early : 0;
     const bool parts = p.kv_parts > 1 || p.q_parts > 1;
-    const auto kernel = parts ? bwd_kernel<D, true, false> : a.parts.joined ? bwd_kernel<D, false, true> : bwd_kernel<D, false, false>;
-    const int bit = 1 << (parts ? 1 : a.parts.joined ? 2 : 0);
+    const int variant = parts ? 1 : a.parts.joined ? 2 : 0, bit = 1 << (variant + (a.split ? 3 : 0));
+    static decltype(&bwd_kernel<D, false, false, false>) const kernels[2][3] = {
+        {bwd_kernel<D, false, false, false>, bwd_kernel<D, true, false, false>, bwd_kernel<D, false, true, false>},
+        {bwd_kernel<D, false, false, true>, bwd_kernel<D, true, false, true>, bwd_kernel<D, false, true, true>}};
+    const auto kernel = kernels[a.split][variant];
     if (!(*a.attributes & bit)) {
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes<D>);
         if (e != cudaSuccess) return e;

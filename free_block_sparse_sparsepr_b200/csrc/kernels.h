@@ -204,6 +204,7 @@ struct AttnBwdArgs {
     int* attributes;                     // host: which kernels' attributes the handle has set (0 at first)
     BwdParts parts;
     int P, g, N, d, Gq, Gk;
+    bool split;                          // dS as two bf16 parts in dQ
 };
 size_t attn_bwd_workspace(int P, int g, int N, int d, int Gq, int Gk, const BwdParts& parts, bool sparse);
 int attn_bwd_launches(const AttnBwdArgs& a);

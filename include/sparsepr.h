@@ -75,6 +75,8 @@ typedef enum sparsepr_status {
                                                       flight, the output rows are written as zeros and the device
                                                       status word reads SPARSEPR_ERR_TIMEOUT; it exercises the
                                                       bounded waits without a fault or a hang */
+#define SPARSEPR_FLAG_BWD_SPLIT_DS      (1u << 10) /* backward passes: dS enters dQ as two bf16 parts (16 bits), an
+                                                      eighth product; dK and dV stay as they are */
 
 /*
  * Shape and hyper-parameters of one call. Defaults used by the page: rK=48,
@@ -368,8 +370,9 @@ sparsepr_status sparsepr_dense_attn_lse(sparsepr_handle h, const void* Q, const 
  * dS = P (dO.v - D): dV = P^T dO, dK = dS^T Q / sqrt(d), dQ = dS K / sqrt(d), dK and dV summed over
  * the query heads that share the KV head. Logits, sums and dS are fp32; P's exponentials are within 2^-18 of
  * their value (0 below 2^-126.5); P and dS are rounded to bf16 as matrix operands; every gradient is
- * rounded to bf16 once. Against fp64 the 2-norm of the error is 2.2e-3 to 3.0e-3 of the gradient's, where rounding
- * the exact gradient to bf16 costs 1.7e-3. Results repeat bit for bit. A row whose lse is -inf is left out: its dQ
+ * rounded to bf16 once. Against fp64 the 2-norm of the error is 2.2e-3 to 2.4e-3 of dK's and dV's and 2.5e-3 to
+ * 3.0e-3 of dQ's, where rounding the exact gradient to bf16 costs 1.7e-3; SPARSEPR_FLAG_BWD_SPLIT_DS brings dQ to
+ * that. Results repeat bit for bit. A row whose lse is -inf is left out: its dQ
  * is 0 and it adds nothing to dK and dV.
  *
  * sparsepr_dense_attn_bwd: Q, K, V, O, lse as sparsepr_dense_attn_lse takes and leaves them, dO the
