@@ -446,8 +446,9 @@ class SparsePR:
         """Gradients of permute followed by blocksparse_attn, with the partition and the route held constant (and of
         writeback without a fit; the correction of one with a fit, or of `attention`, has no gradient here):
         group-major Qp, Kp, Vp, Osp, lse and dOsp in (dOsp: permute of the original-order gradient), dQ, dK
-        and dV in the original token order out. workspace: attn_bwd_workspace_bytes(). A partition or route whose buffers the handle owns is
-        overwritten by the handle's next call: keep copies (partition_views, route_views) across calls."""
+        and dV in the original token order out. workspace: attn_bwd_workspace_bytes(). A partition or route
+        whose buffers the handle owns is overwritten by the handle's next call: keep copies (partition_views,
+        route_views) across calls."""
         return self._bwd("sparsepr_blocksparse_attn_bwd",
                          lambda q, k, v, *a: self.lib.sparsepr_blocksparse_attn_bwd(
                              self.h, q, k, v, ctypes.byref(part), ctypes.byref(route), *a),
