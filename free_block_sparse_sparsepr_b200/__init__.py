@@ -27,6 +27,7 @@ FLAG_PROBES_RANDOM = 1 << 6      # ablation: probes drawn at random (seeded Spli
 FLAG_SEMANTIC_PARTITION = 1 << 7  # ablation: k-means on the raw keys and the raw mean query
 FLAG_STAGE_TIMING = 1 << 8
 FLAG_TEST_STALL = 1 << 9          # test only: the dense kernel's first bounded wait runs out
+FLAG_TEST_STALL_BWD = 1 << 11     # test only: the same for the backward passes' kernel
 FLAG_BWD_SPLIT_DS = 1 << 10       # backward passes: dS as two bf16 parts in dQ, at the price of an eighth product
 
 STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported configuration", 3: "workspace allocation failed",

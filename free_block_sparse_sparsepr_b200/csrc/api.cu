@@ -23,7 +23,7 @@ constexpr unsigned kSupportedFlags =
     SPARSEPR_FLAG_HARD_DROP_ONLY | SPARSEPR_FLAG_RIDGE_ONLY | SPARSEPR_FLAG_RBAR_UNPROJECTED |
     SPARSEPR_FLAG_UNIFORM_WEIGHTS | SPARSEPR_FLAG_TOPMASS | SPARSEPR_FLAG_STAGE_TIMING |
     SPARSEPR_FLAG_PROBES_UNIFORM | SPARSEPR_FLAG_PROBES_RANDOM | SPARSEPR_FLAG_SEMANTIC_PARTITION |
-    SPARSEPR_FLAG_TEST_STALL | SPARSEPR_FLAG_BWD_SPLIT_DS;
+    SPARSEPR_FLAG_TEST_STALL | SPARSEPR_FLAG_BWD_SPLIT_DS | SPARSEPR_FLAG_TEST_STALL_BWD;
 
 inline int pad16(int v) { return (v + 15) / 16 * 16; }
 inline int pad64(int v) { return (v + 63) / 64 * 64; }
@@ -992,6 +992,7 @@ sparsepr_status attn_bwd_impl(sparsepr_handle h, const void* Q, const void* K, c
     a.attributes = &h->bwd_attributes;
     a.parts = h->bwd_parts[route != nullptr];
     a.split = (c.flags & SPARSEPR_FLAG_BWD_SPLIT_DS) != 0;
+    a.stall = (c.flags & SPARSEPR_FLAG_TEST_STALL_BWD) != 0;
     a.P = h->P; a.g = h->g; a.N = c.N; a.d = c.d; a.Gq = c.Gq; a.Gk = c.Gk;
     if (route) {
         a.qperm = part->qperm; a.kperm = part->kperm; a.qoff = part->qoff; a.koff = part->koff;

@@ -50,10 +50,11 @@ struct BwdParams {
     int kv_tiles, q_tiles;                  // most key tiles of a KV head, query tiles of a query head
     int kv_parts, q_parts;                  // CTAs that share a tile's stream
     float *kv_part, *q_part;                // their fp32 sums: [part][dV, dK][P N][D], [part][P g N][D]
-    const int32_t* loose;                   // [P][query groups, key groups]: whether their offsets leave rows out (null: dense)
     int kv_blocks;                          // CTAs of dK and dV
     int kv_first, q_early;                  // launch order: so many of dK and dV, so many of dQ, then the others of each
     float scale, scale_log2;
+    const int32_t* loose;                   // [P][query groups, key groups]: whether their offsets leave rows out (null: dense)
+    int stall;                              // test only: the tile that a CTA owns is not loaded, so that the wait for it runs out
 };
 
 // Tensor maps of [rows][64] boxes of 128 rows.
@@ -799,6 +800,7 @@ __device__ __forceinline__ void dkv_tile(const BwdMaps& m, const BwdParams& p, u
     const Cta c = cta_setup<D>(
         smem_raw, kOffBar, kBars, p.status, [](int i) { return i >= kSread ? W::kArrivals : i >= kQf && i < kOf ? 2 : 1; },
         [&](const Cta& c) {
+            if (p.stall) return;
             tc::mbar_arrive_expect_tx(c.bar(kKV), 2 * (D / 64) * kRegion);
             for (int h = 0; h < D / 64; ++h) {
                 tc::tma_load_2d(c.base + kOffK + h * kRegion, &m.k, c.bar(kKV), 64 * h, z * p.N + klo);
@@ -856,7 +858,7 @@ __device__ __forceinline__ void dkv_tile(const BwdMaps& m, const BwdParams& p, u
         int never = 0;
         for (int i = max(0, nq - kStages); i < nq; ++i) tc::mbar_wait(c.bar(kQf + i % kStages), (i / kStages) & 1, &never);
         for (int i = max(0, no - kStages); i < no; ++i) tc::mbar_wait(c.bar(kOf + i % kStages), (i / kStages) & 1, &never);
-        tc::mbar_wait(c.bar(kKV), 0, &never);
+        if (!p.stall) tc::mbar_wait(c.bar(kKV), 0, &never);
     } else if (c.warp == W::kMma) {
         const uint32_t go = tc::elect_one();
         auto wait = [&](int b, int parity) {
@@ -1047,6 +1049,7 @@ __device__ __forceinline__ void dq_tile(const BwdMaps& m, const BwdParams& p, un
     const Cta c = cta_setup<D>(
         smem_raw, kOffBar, kBars, p.status, [](int i) { return i >= kSread ? W::kArrivals : 1; },
         [&](const Cta& c) {
+            if (p.stall) return;
             tc::mbar_arrive_expect_tx(c.bar(kQO), 2 * (D / 64) * kRegion);
             for (int h = 0; h < D / 64; ++h) {
                 tc::tma_load_2d(c.base + kOffQ + h * kRegion, &m.q, c.bar(kQO), 64 * h, x * p.N + qlo);
@@ -1074,7 +1077,7 @@ __device__ __forceinline__ void dq_tile(const BwdMaps& m, const BwdParams& p, un
         int never = 0;
         for (int i = max(0, nk - kKStages); i < nk; ++i) tc::mbar_wait(c.bar(kKf + i % kKStages), (i / kKStages) & 1, &never);
         for (int i = max(0, nv - kVStages); i < nv; ++i) tc::mbar_wait(c.bar(kVf + i % kVStages), (i / kVStages) & 1, &never);
-        tc::mbar_wait(c.bar(kQO), 0, &never);
+        if (!p.stall) tc::mbar_wait(c.bar(kQO), 0, &never);
     } else if (c.warp == W::kMma) {
         const uint32_t go = tc::elect_one();
         auto wait = [&](int b, int parity) {
@@ -1312,6 +1315,7 @@ cudaError_t launch_bwd(const AttnBwdArgs& a, cudaStream_t s) {
     p.kv_parts = a.parts.kv; p.q_parts = a.parts.q;
     p.kv_part = reinterpret_cast<float*>(ws + l.kv_part); p.q_part = reinterpret_cast<float*>(ws + l.q_part);
     p.status = a.status;
+    p.stall = a.stall;
     p.scale = (float)(1.0 / sqrt((double)D));
     p.scale_log2 = (float)(1.4426950408889634 / sqrt((double)D));
     const int tiles = (a.N + kTile - 1) / kTile;

@@ -205,6 +205,7 @@ struct AttnBwdArgs {
     BwdParts parts;
     int P, g, N, d, Gq, Gk;
     bool split;                          // dS as two bf16 parts in dQ
+    bool stall;                          // test only: the wait for the tile that a CTA owns runs out
 };
 size_t attn_bwd_workspace(int P, int g, int N, int d, int Gq, int Gk, const BwdParts& parts, bool sparse);
 int attn_bwd_launches(const AttnBwdArgs& a);

@@ -77,6 +77,9 @@ typedef enum sparsepr_status {
                                                       bounded waits without a fault or a hang */
 #define SPARSEPR_FLAG_BWD_SPLIT_DS      (1u << 10) /* backward passes: dS enters dQ as two bf16 parts (16 bits), an
                                                       eighth product; dK and dV stay as they are */
+#define SPARSEPR_FLAG_TEST_STALL_BWD    (1u << 11) /* TEST ONLY: the same as SPARSEPR_FLAG_TEST_STALL for the kernel of
+                                                      the backward passes: a CTA does not load the tile that it owns, the
+                                                      wait for it runs out and the tile's rows stay unwritten */
 
 /*
  * Shape and hyper-parameters of one call. Defaults used by the page: rK=48,

@@ -3,6 +3,7 @@ offsets leave out, non-finite values in operands that a gradient does not read, 
 directional differences along the gradients themselves."""
 import ctypes
 import math
+import time
 
 import pytest
 
@@ -287,3 +288,48 @@ def test_a_dense_call_needs_no_room_for_lists():
 def test_null_workspace_queries_without_gpu():
     n = ctypes.c_size_t()
     assert spr.load_library().sparsepr_dense_attn_bwd_workspace(None, ctypes.byref(n)) == 1
+
+
+@gpu
+@pytest.mark.parametrize("shape", [(1, 1, 1, 640, 128), (4, 40, 40, 100, 128), (4, 40, 40, 100, 64), (1, 3, 1, 300, 64)], ids=str)
+@pytest.mark.parametrize("side", ["both", "dQ", "dK and dV"])
+def test_a_wait_of_the_backward_kernel_runs_out(shape, side):
+    """The tile that a CTA owns is never loaded: the wait for it gives up after about two seconds, the streamed tiles on
+    their way land, every CTA returns, nothing is written, the status says so, and another handle's call runs clean."""
+    _need_gpu()
+    B, Hq, Hkv, N, d = shape
+    Q, K, V, dO = _inputs(17, *shape)
+    O, lse = forward_reference(Q, K, V)
+    args = (Q, K, V, O.bfloat16(), lse.float(), dO)
+    out = _filled(Q, K, V)
+    kw = {"both": dict(dQ=out[0], dK=out[1], dV=out[2]), "dQ": dict(dQ=out[0], need_dkv=False),
+          "dK and dV": dict(dK=out[1], dV=out[2], need_dq=False)}[side]
+    with spr.SparsePR(B, Hq, Hkv, N, d, Gk=1, Gq=1, flags=spr.FLAG_HARD_DROP_ONLY | spr.FLAG_TEST_STALL_BWD) as h:
+        t0 = time.perf_counter()
+        h.dense_attn_bwd(*args, **kw, workspace=_workspace(h))
+        torch.cuda.synchronize()
+        assert time.perf_counter() - t0 < 60.0
+        assert h.device_status() == 5 and h.device_status() == 0
+    assert all((x == 7).all() for x in out)
+    with _handle(*shape) as h:
+        got = h.dense_attn_bwd(*args)
+        torch.cuda.synchronize()
+        assert h.device_status() == 0
+    check_gradients(got, backward_reference(*args), f"after a stalled call {shape}")
+
+
+@gpu
+@pytest.mark.parametrize("shape,G", [((1, 8, 1, 700, 128), 12), ((4, 40, 20, 400, 64), 4)], ids=str)
+def test_a_wait_of_the_routed_backward_kernel_runs_out(shape, G):
+    """Shared streams, and tiles of two groups; every group keeps some cell."""
+    _need_gpu()
+    B, Hq, Hkv, N, d = shape
+    Q, K, V, dO = _inputs(18, *shape)
+    t, masks = _routed(18, B * Hkv, N, G, G, 1.0)
+    O, lse = forward_reference(Q, K, V, masks)
+    out = _filled(Q, K, V)
+    with spr.SparsePR(B, Hq, Hkv, N, d, Gk=G, Gq=G, flags=spr.FLAG_HARD_DROP_ONLY | spr.FLAG_TEST_STALL_BWD) as h:
+        h.blocksparse_attn_bwd(Q, K, V, *_structs(t), O.bfloat16(), lse.float(), dO, *out, workspace=_workspace(h))
+        torch.cuda.synchronize()
+        assert h.device_status() == 5
+    assert all((x == 7).all() for x in out)
